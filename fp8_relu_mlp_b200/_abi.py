@@ -30,6 +30,7 @@ ERR_NO_DEVICE = 5
 STATUS_TIMEOUT = 1
 STATUS_NONFINITE_AMAX = 2
 STATUS_W2_DEGENERATE = 4
+STATUS_STEP_SKIPPED = 8
 STATE_KEPT_SCALE = 1
 FWD_EVAL_BF16 = 1
 FWD_CALIBRATE = 2
@@ -50,6 +51,7 @@ class Fp8MlpError(RuntimeError):
 
 
 _i, _u64, _f, _p, _sz = ctypes.c_int, ctypes.c_ulonglong, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_u32 = ctypes.c_uint32
 
 _SIGS = {
     "fp8mlp_up_proj_fused": [_i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _p],
@@ -82,6 +84,17 @@ _SIGS = {
     "fp8mlp_rmsnorm_fwd_quant": [_i, _i, _p, _p, _p, _p, _p, _p, _p],
     "fp8mlp_rmsnorm_bwd": [_i, _i, _p, _p, _p, _p, _p, _p],
     "fp8mlp_residual_add": [_i, _i, _p, _p, _p, _p],
+    "fp8mlp_quantize_block": [_i, _i, _p, _p, _p, _p],
+    "fp8mlp_weight_block_cache_refresh": [_i, _i, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_linear_fwd_block": [_i, _i, _i, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_linear_block": [_i, _i, _i, _p, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_up_proj_block": [_i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_mlp_fwd_block": [_i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_norm_gate_fwd": [_i, _i, _p, _p, _p, _p, _i, _p, _p, _f, _p, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_norm_gate_bwd": [_i, _i, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p],
+    "fp8mlp_adamw_state_init": [_p, _f, _u32, _i, _p],
+    "fp8mlp_grad_norm": [_i, _p, _f, _p, _p, _p],
+    "fp8mlp_adamw_step": [_i, _p, _p, _i, _f, _f, _f, _p, _p],
     "fp8mlp_get_device_status": [_p, _p],
     "fp8mlp_clear_device_status": [_p],
     "fp8mlp_set_wait_timeout_ns": [_u64],
@@ -98,6 +111,10 @@ lib.fp8mlp_ce_workspace_size.argtypes = [_i, _i, _i]
 lib.fp8mlp_ce_workspace_size.restype = _sz
 lib.fp8mlp_linear_bwd_workspace_size.argtypes = [_i, _i, _i]
 lib.fp8mlp_linear_bwd_workspace_size.restype = _sz
+lib.fp8mlp_norm_gate_bwd_workspace_size.argtypes = [_i, _i, _i]
+lib.fp8mlp_norm_gate_bwd_workspace_size.restype = _sz
+lib.fp8mlp_grad_norm_workspace_size.argtypes = [_i, _p]
+lib.fp8mlp_grad_norm_workspace_size.restype = _sz
 lib.fp8mlp_kernel_launch_count.argtypes = []
 lib.fp8mlp_kernel_launch_count.restype = ctypes.c_ulonglong
 for _n in ("fp8mlp_error_string",):
@@ -333,6 +350,152 @@ def fp8mlp_rmsnorm_bwd(M, d, r, rstd, dx, dr_in, dr_out, stream=None):
 
 def fp8mlp_residual_add(M, d, r, out, r_next, stream=None):
     return _call("fp8mlp_residual_add", M, d, _ptr(r), _ptr(out), _ptr(r_next), _stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# block-scaled FP8 products, gated norms, optimizer.  Tensors of these calls
+# are also held to their sizes and to the current device: a kernel that is
+# handed a short buffer, or one of another GPU, would write out of bounds.
+# ---------------------------------------------------------------------------
+
+def _buf(t, need, name):
+    """Device address of ``t`` with at least ``need`` bytes (None stays NULL;
+    an int is an address the caller vouches for)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name}: cannot pass {type(t)} as a pointer")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor arguments must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
+    if t.nbytes < need:
+        raise ValueError(f"{name}: {need} bytes are needed, the tensor has {t.nbytes}")
+    return t.data_ptr()
+
+
+def _kblocks(n):
+    return -(-n // 128)
+
+
+def fp8mlp_quantize_block(M, K, x, xq, xs, stream=None):
+    return _call("fp8mlp_quantize_block", M, K, _buf(x, 2 * M * K, "x"), _buf(xq, M * K, "xq"),
+                 _buf(xs, 4 * M * _kblocks(K), "xs"), _stream(stream))
+
+
+def fp8mlp_weight_block_cache_refresh(N, K, W, Wq, ws, Wq_t=None, ws_t=None, stream=None):
+    sc = 4 * _kblocks(K) * _kblocks(N)
+    return _call("fp8mlp_weight_block_cache_refresh", N, K, _buf(W, 2 * N * K, "W"), _buf(Wq, N * K, "Wq"),
+                 _buf(ws, sc, "ws"), _buf(Wq_t, N * K, "Wq_t"), _buf(ws_t, sc, "ws_t"), _stream(stream))
+
+
+def fp8mlp_linear_fwd_block(M, K, N, xq, xs, Wq, ws, y, stream=None):
+    kb = _kblocks(K)
+    return _call("fp8mlp_linear_fwd_block", M, K, N, _buf(xq, M * K, "xq"), _buf(xs, 4 * M * kb, "xs"),
+                 _buf(Wq, N * K, "Wq"), _buf(ws, 4 * kb * _kblocks(N), "ws"), _buf(y, 2 * M * N, "y"),
+                 _stream(stream))
+
+
+def fp8mlp_linear_block(M, K, N, x, Wq, ws, xq, xs, y, stream=None):
+    kb = _kblocks(K)
+    return _call("fp8mlp_linear_block", M, K, N, _buf(x, 2 * M * K, "x"), _buf(Wq, N * K, "Wq"),
+                 _buf(ws, 4 * kb * _kblocks(N), "ws"), _buf(xq, M * K, "xq"), _buf(xs, 4 * M * kb, "xs"),
+                 _buf(y, 2 * M * N, "y"), _stream(stream))
+
+
+def fp8mlp_up_proj_block(M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, stream=None):
+    kd, kh = _kblocks(d), _kblocks(h)
+    return _call("fp8mlp_up_proj_block", M, d, h, _buf(xq, M * d, "xq"), _buf(xs, 4 * M * kd, "xs"),
+                 _buf(W1q, h * d, "W1q"), _buf(w1s, 4 * kd * kh, "w1s"), _buf(post, 2 * M * h, "post"),
+                 _buf(post_q, M * h, "post_q"), _buf(post_s, 4 * M * kh, "post_s"), _stream(stream))
+
+
+def fp8mlp_mlp_fwd_block(M, d, h, x, W1q, w1s, W2q_t, w2s_t, xq, xs, post, post_q, post_s, out, stream=None):
+    kd, kh = _kblocks(d), _kblocks(h)
+    return _call("fp8mlp_mlp_fwd_block", M, d, h, _buf(x, 2 * M * d, "x"), _buf(W1q, h * d, "W1q"),
+                 _buf(w1s, 4 * kd * kh, "w1s"), _buf(W2q_t, h * d, "W2q_t"), _buf(w2s_t, 4 * kd * kh, "w2s_t"),
+                 _buf(xq, M * d, "xq"), _buf(xs, 4 * M * kd, "xs"), _buf(post, 2 * M * h, "post"),
+                 _buf(post_q, M * h, "post_q"), _buf(post_s, 4 * M * kh, "post_s"), _buf(out, 2 * M * d, "out"),
+                 _stream(stream))
+
+
+def _gate_rows(M, rows_per_gate):
+    return -(-M // rows_per_gate) if rows_per_gate > 0 else 0
+
+
+def fp8mlp_norm_gate_fwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, w_pre, eps, r_next, rstd_post, x, rstd_pre,
+                         xq=None, xs=None, stream=None):
+    n = 2 * M * d
+    return _call("fp8mlp_norm_gate_fwd", M, d, _buf(r, n, "r"), _buf(y, n, "y"), _buf(w_post, 2 * d, "w_post"),
+                 _buf(gate, 2 * d * _gate_rows(M, rows_per_gate), "gate"), rows_per_gate, _buf(alpha, 4, "alpha"),
+                 _buf(w_pre, 2 * d, "w_pre"), eps, _buf(r_next, n, "r_next"), _buf(rstd_post, 4 * M, "rstd_post"),
+                 _buf(x, n, "x"), _buf(rstd_pre, 4 * M, "rstd_pre"), _buf(xq, M * d, "xq"),
+                 _buf(xs, 4 * M * _kblocks(d), "xs"), _stream(stream))
+
+
+def fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate):
+    return int(lib.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate))
+
+
+def fp8mlp_norm_gate_bwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, rstd_post, r_next, w_pre, rstd_pre, dx,
+                         dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, workspace, stream=None):
+    n, g = 2 * M * d, _gate_rows(M, rows_per_gate)
+    need = int(lib.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate))
+    return _call("fp8mlp_norm_gate_bwd", M, d, _buf(r, n, "r"), _buf(y, n, "y"), _buf(w_post, 2 * d, "w_post"),
+                 _buf(gate, 2 * d * g, "gate"), rows_per_gate, _buf(alpha, 4, "alpha"),
+                 _buf(rstd_post, 4 * M, "rstd_post"), _buf(r_next, n, "r_next"), _buf(w_pre, 2 * d, "w_pre"),
+                 _buf(rstd_pre, 4 * M, "rstd_pre"), _buf(dx, n, "dx"), _buf(dr_next, n, "dr_next"), _buf(dr, n, "dr"),
+                 _buf(dy, n, "dy"), _buf(dw_post, 4 * d, "dw_post"), _buf(dgate, 4 * d * g, "dgate"),
+                 _buf(dalpha, 4, "dalpha"), _buf(dw_pre, 4 * d, "dw_pre"), _buf(workspace, need, "workspace"),
+                 _stream(stream))
+
+
+class AdamwTensor(ctypes.Structure):
+    """fp8mlp_adamw_tensor"""
+    _fields_ = [("n", ctypes.c_int64), ("p", _p), ("p_bf16", _p), ("g", _p), ("m", _p), ("v", _p), ("m_scale", _p),
+                ("v_scale", _p), ("lr_mult", _f), ("weight_decay", _f)]
+
+
+def adamw_tensor(n, p, p_bf16, g, m, v, m_scale=None, v_scale=None, lr_mult=1.0, weight_decay=0.0, state_bits=32):
+    """One descriptor for :func:`fp8mlp_adamw_step`, its tensors' sizes checked.
+    It holds addresses: the tensors have to stay alive."""
+    sb, nb = state_bits // 8, 4 * _kblocks(n)
+    return AdamwTensor(n, _buf(p, 4 * n, "p"), _buf(p_bf16, 2 * n, "p_bf16"), _buf(g, 4 * n, "g"),
+                       _buf(m, sb * n, "m"), _buf(v, sb * n, "v"), _buf(m_scale, nb, "m_scale"),
+                       _buf(v_scale, nb, "v_scale"), lr_mult, weight_decay)
+
+
+def adamw_tensors(descriptors):
+    """The array the calls below take; build it once, use it every step."""
+    return (AdamwTensor * len(descriptors))(*descriptors)
+
+
+def _tensors(arr):
+    if not isinstance(arr, ctypes.Array) or arr._type_ is not AdamwTensor:
+        raise TypeError("tensors: an array from adamw_tensors() is needed")
+    return len(arr), ctypes.addressof(arr)
+
+
+def fp8mlp_adamw_state_init(st, lr, seed=0, step=0, stream=None):
+    return _call("fp8mlp_adamw_state_init", _buf(st, 32, "st"), lr, seed, step, _stream(stream))
+
+
+def fp8mlp_grad_norm_workspace_size(tensors):
+    return int(lib.fp8mlp_grad_norm_workspace_size(*_tensors(tensors)))
+
+
+def fp8mlp_grad_norm(tensors, max_norm, norm_coef, workspace, stream=None):
+    need = int(lib.fp8mlp_grad_norm_workspace_size(*_tensors(tensors)))
+    return _call("fp8mlp_grad_norm", *_tensors(tensors), max_norm, _buf(norm_coef, 8, "norm_coef"),
+                 _buf(workspace, need, "workspace"), _stream(stream))
+
+
+def fp8mlp_adamw_step(tensors, st, state_bits, beta1, beta2, eps, grad_coef=None, stream=None):
+    return _call("fp8mlp_adamw_step", *_tensors(tensors), _buf(st, 32, "st"), state_bits, beta1, beta2, eps,
+                 _buf(grad_coef, 4, "grad_coef"), _stream(stream))
 
 
 def fp8mlp_get_device_status(stream=None):

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <string>
 
+#include "block.h"
 #include "internal.h"
 
 #define FP8MLP_VERSION_STRING "fp8mlp 0.1.0 (sm_100a)"
@@ -962,6 +963,340 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
   TRY(current_device(&di));
   const cudaError_t e = launch_residual_add(M, d, r, out, r_next, di->num_sms, stream);
   return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "residual_add launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- block-scaled FP8 products ----------------------------------------------
+int block_product(bool relu2, int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
+                  const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di,
+                  cudaStream_t stream) {
+  BlockGemmParams p{};
+  const bool pairs = block_gemm_pairs(M, N, di->num_sms);
+  TRY(map_kmajor(&p.tmA, xq, U8, 1, M, K, kGemmBM, "xq"));
+  TRY(map_kmajor(&p.tmB, Wq, U8, 1, N, K, 128, "Wq"));
+  TRY(map_tile32(&p.tmOut, out, BF16, 2, M, N, "output"));
+  if (relu2) TRY(map_tile32(&p.tmOut2, post_q, U8, 1, M, N, "post_q"));
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.n_blocks = cdiv(N, kBlock);
+  p.xs = xs;
+  p.ws = ws;
+  p.post_s = post_s;
+  p.status = di->status;
+  p.timeout_ns = g_timeout_ns.load();
+  p.debug_flags = g_debug_flags.load();
+  const cudaError_t e = launch_block_gemm(relu2, pairs, p, di->num_sms, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, relu2 ? "up_proj_block launch" : "linear_fwd_block launch");
+}
+
+int quantize_rows(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, cudaStream_t stream) {
+  const cudaError_t e = launch_quantize_block(M, K, x, xq, xs, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "quantize_block launch");
+}
+
+int check_adamw_tensors(int n, const fp8mlp_adamw_tensor* t) {
+  if (n < 0) return fail(FP8MLP_ERR_INVALID_ARG, "n_tensors < 0");
+  if (n > 0 && t == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "tensors is NULL");
+  long long chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n < 0) return fail(FP8MLP_ERR_INVALID_ARG, "a tensor's n < 0");
+    if (t[i].n == 0) continue;
+    const float* g = t[i].g;
+    REQUIRE_PTR(g);
+    // chunks of 4096 elements are counted in 32 bits
+    if (t[i].n > (1ll << 42)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "a tensor's n is above 2^42");
+    chunks += (t[i].n + 4095) / 4096;
+    if (chunks > 0x7FFFFFFFll) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "too many elements in one call");
+  }
+  return FP8MLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, K, 16));
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(xq);
+  REQUIRE_PTR4(xs);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  return quantize_rows(M, K, x, xq, xs, stream);
+}
+
+int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t,
+                                      float* ws_t, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(0, N, K));
+  if (N > (1 << 22) || K > (1 << 22)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "N and K must be <= 2^22");
+  REQUIRE_PTR(W);
+  if (Wq == nullptr && Wq_t == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "Wq and Wq_t are both NULL");
+  if ((Wq == nullptr) != (ws == nullptr) || (Wq_t == nullptr) != (ws_t == nullptr))
+    return fail(FP8MLP_ERR_INVALID_ARG, "codes and scales come in pairs");
+  if (Wq != nullptr) {
+    REQUIRE_PTR(Wq);
+    REQUIRE_PTR4(ws);
+  }
+  if (Wq_t != nullptr) {
+    REQUIRE_PTR(Wq_t);
+    REQUIRE_PTR4(ws_t);
+  }
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const cudaError_t e = launch_weight_block(N, K, W, Wq, ws, Wq_t, ws_t, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "weight_block_cache_refresh launch");
+}
+
+int fp8mlp_linear_fwd_block(int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
+                            const float* ws, uint16_t* y, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, N, K));
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(xq);
+  REQUIRE_PTR4(xs);
+  REQUIRE_PTR(Wq);
+  REQUIRE_PTR4(ws);
+  REQUIRE_PTR(y);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  return block_product(false, M, K, N, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
+}
+
+int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* Wq, const float* ws, uint8_t* xq,
+                        float* xs, uint16_t* y, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, N, K));
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(Wq);
+  REQUIRE_PTR4(ws);
+  REQUIRE_PTR(xq);
+  REQUIRE_PTR4(xs);
+  REQUIRE_PTR(y);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  TRY(quantize_rows(M, K, x, xq, xs, stream));
+  return block_product(false, M, K, N, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
+}
+
+int fp8mlp_up_proj_block(int M, int d, int h, const uint8_t* xq, const float* xs, const uint8_t* W1q,
+                         const float* w1s, uint16_t* post, uint8_t* post_q, float* post_s, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, d, h));
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(xq);
+  REQUIRE_PTR4(xs);
+  REQUIRE_PTR(W1q);
+  REQUIRE_PTR4(w1s);
+  REQUIRE_PTR(post);
+  REQUIRE_PTR(post_q);
+  REQUIRE_PTR4(post_s);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  return block_product(true, M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, di, stream);
+}
+
+int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* W1q, const float* w1s,
+                         const uint8_t* W2q_t, const float* w2s_t, uint8_t* xq, float* xs, uint16_t* post,
+                         uint8_t* post_q, float* post_s, uint16_t* out, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, d, h));
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(W1q);
+  REQUIRE_PTR4(w1s);
+  REQUIRE_PTR(W2q_t);
+  REQUIRE_PTR4(w2s_t);
+  REQUIRE_PTR(xq);
+  REQUIRE_PTR4(xs);
+  REQUIRE_PTR(post);
+  REQUIRE_PTR(post_q);
+  REQUIRE_PTR4(post_s);
+  REQUIRE_PTR(out);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  TRY(quantize_rows(M, d, x, xq, xs, stream));
+  TRY(block_product(true, M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, di, stream));
+  return block_product(false, M, h, d, post_q, post_s, W2q_t, w2s_t, out, nullptr, nullptr, di, stream);
+}
+
+// ---- norms with gate and residual scale ---------------------------------------
+int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
+                         const uint16_t* gate, int rows_per_gate, const float* alpha, const uint16_t* w_pre, float eps,
+                         uint16_t* r_next, float* rstd_post, uint16_t* x, float* rstd_pre, uint8_t* xq, float* xs,
+                         fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, d, 16));
+  if (d > kNormMaxD) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "d must be <= 8192");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(FP8MLP_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (rows_per_gate < 1) return fail(FP8MLP_ERR_INVALID_ARG, "rows_per_gate < 1");
+  if ((xq == nullptr) != (xs == nullptr)) return fail(FP8MLP_ERR_INVALID_ARG, "xq and xs come as a pair");
+  if (M == 0) return FP8MLP_OK;
+  REQUIRE_PTR(r);
+  if (y == nullptr && x == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "y and x are both NULL");
+  if (y != nullptr) {
+    REQUIRE_PTR(y);
+    REQUIRE_PTR(r_next);
+    REQUIRE_PTR4(rstd_post);
+    if (w_post != nullptr) REQUIRE_PTR(w_post);
+    if (gate != nullptr) REQUIRE_PTR(gate);
+    if (alpha != nullptr) REQUIRE_PTR4(alpha);
+  } else if (w_post != nullptr || gate != nullptr || alpha != nullptr || r_next != nullptr || rstd_post != nullptr) {
+    return fail(FP8MLP_ERR_INVALID_ARG, "w_post, gate, alpha, r_next and rstd_post go with y");
+  }
+  if (x != nullptr) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR4(rstd_pre);
+    if (w_pre != nullptr) REQUIRE_PTR(w_pre);
+    if (xq != nullptr) {
+      REQUIRE_PTR(xq);
+      REQUIRE_PTR4(xs);
+    }
+  } else if (w_pre != nullptr || rstd_pre != nullptr || xq != nullptr) {
+    return fail(FP8MLP_ERR_INVALID_ARG, "w_pre, rstd_pre, xq and xs go with x");
+  }
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const NormGateFwd p{M, d, rows_per_gate, eps, r, y, w_post, gate, w_pre, alpha, r_next, x, rstd_post, rstd_pre, xq, xs};
+  const cudaError_t e = launch_norm_gate_fwd(p, di->num_sms, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "norm_gate_fwd launch");
+}
+
+size_t fp8mlp_norm_gate_bwd_workspace_size(int M, int d, int rows_per_gate) {
+  if (M <= 0 || d <= 0 || rows_per_gate <= 0) return 0;
+  return norm_gate_bwd_workspace(M, d, rows_per_gate);
+}
+
+int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
+                         const uint16_t* gate, int rows_per_gate, const float* alpha, const float* rstd_post,
+                         const uint16_t* r_next, const uint16_t* w_pre, const float* rstd_pre, const uint16_t* dx,
+                         const uint16_t* dr_next, uint16_t* dr, uint16_t* dy, float* dw_post, float* dgate,
+                         float* dalpha, float* dw_pre, void* workspace, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_dims(M, d, 16));
+  if (d > kNormMaxD) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "d must be <= 8192");
+  if (rows_per_gate < 1) return fail(FP8MLP_ERR_INVALID_ARG, "rows_per_gate < 1");
+  if (dw_post != nullptr) REQUIRE_PTR(dw_post);
+  if (dw_pre != nullptr) REQUIRE_PTR(dw_pre);
+  if (dgate != nullptr) REQUIRE_PTR(dgate);
+  if (dalpha != nullptr) REQUIRE_PTR4(dalpha);
+  if (M == 0) {
+    // an empty batch contributes zero gradient
+    DeviceInfo* di = nullptr;
+    TRY(current_device(&di));
+    cudaError_t e = cudaSuccess;
+    if (dw_post != nullptr) e = cudaMemsetAsync(dw_post, 0, sizeof(float) * d, stream);
+    if (e == cudaSuccess && dw_pre != nullptr) e = cudaMemsetAsync(dw_pre, 0, sizeof(float) * d, stream);
+    if (e == cudaSuccess && dalpha != nullptr) e = cudaMemsetAsync(dalpha, 0, sizeof(float), stream);
+    return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "norm_gate_bwd memset");
+  }
+  if (y == nullptr && dx == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "y and dx are both NULL");
+  REQUIRE_PTR(dr);
+  if (dr_next != nullptr) REQUIRE_PTR(dr_next);
+  if (y != nullptr) {
+    REQUIRE_PTR(y);
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR4(rstd_post);
+    if (w_post != nullptr) REQUIRE_PTR(w_post);
+    if (gate != nullptr) REQUIRE_PTR(gate);
+    if (alpha != nullptr) REQUIRE_PTR4(alpha);
+    if (dalpha != nullptr) REQUIRE_PTR(r);
+  } else if (w_post != nullptr || gate != nullptr || alpha != nullptr || rstd_post != nullptr || dy != nullptr ||
+             dw_post != nullptr || dgate != nullptr || dalpha != nullptr) {
+    return fail(FP8MLP_ERR_INVALID_ARG, "w_post, gate, alpha, rstd_post, dy, dw_post, dgate and dalpha go with y");
+  }
+  if (dx != nullptr) {
+    REQUIRE_PTR(dx);
+    REQUIRE_PTR(r_next);
+    REQUIRE_PTR4(rstd_pre);
+    if (w_pre != nullptr) REQUIRE_PTR(w_pre);
+  } else if (w_pre != nullptr || rstd_pre != nullptr || dw_pre != nullptr) {
+    return fail(FP8MLP_ERR_INVALID_ARG, "w_pre, rstd_pre and dw_pre go with dx");
+  }
+  REQUIRE_PTR(workspace);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const NormGateBwd p{M,  d,       rows_per_gate, r,  y,  w_post,  gate,  w_pre,  alpha,  rstd_post,
+                      rstd_pre, r_next, dx, dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, static_cast<float*>(workspace)};
+  const cudaError_t e = launch_norm_gate_bwd(p, di->num_sms, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "norm_gate_bwd launch");
+}
+
+// ---- optimizer ------------------------------------------------------------------
+int fp8mlp_adamw_state_init(fp8mlp_adamw_state* st, float lr, uint32_t seed, int step, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  REQUIRE_PTR(st);
+  if (!std::isfinite(lr)) return fail(FP8MLP_ERR_INVALID_ARG, "lr must be finite");
+  if (step < 0) return fail(FP8MLP_ERR_INVALID_ARG, "step < 0");
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const cudaError_t e = launch_adamw_state_init(st, lr, seed, step, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "adamw_state_init launch");
+}
+
+size_t fp8mlp_grad_norm_workspace_size(int n_tensors, const fp8mlp_adamw_tensor* tensors) {
+  if (n_tensors <= 0 || tensors == nullptr) return 16;
+  for (int i = 0; i < n_tensors; ++i)
+    if (tensors[i].n < 0) return 0;
+  const size_t n = grad_norm_workspace(n_tensors, tensors);
+  return n < 16 ? 16 : n;
+}
+
+int fp8mlp_grad_norm(int n_tensors, const fp8mlp_adamw_tensor* tensors, float max_norm, float* norm_coef,
+                     void* workspace, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_adamw_tensors(n_tensors, tensors));
+  if (!(max_norm > 0.f)) return fail(FP8MLP_ERR_INVALID_ARG, "max_norm must be > 0");
+  REQUIRE_PTR4(norm_coef);
+  REQUIRE_PTR(workspace);
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const cudaError_t e =
+      launch_grad_norm(n_tensors, tensors, max_norm, norm_coef, static_cast<double*>(workspace), stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "grad_norm launch");
+}
+
+int fp8mlp_adamw_step(int n_tensors, const fp8mlp_adamw_tensor* tensors, fp8mlp_adamw_state* st, int state_bits,
+                      float beta1, float beta2, float eps, const float* grad_coef, fp8mlp_stream_t stream) {
+  g_detail.clear();
+  TRY(check_adamw_tensors(n_tensors, tensors));
+  REQUIRE_PTR(st);
+  if (state_bits != 32 && state_bits != 8) return fail(FP8MLP_ERR_INVALID_ARG, "state_bits must be 32 or 8");
+  if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f))
+    return fail(FP8MLP_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(FP8MLP_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (grad_coef != nullptr) REQUIRE_PTR4(grad_coef);
+  for (int i = 0; i < n_tensors; ++i) {
+    const fp8mlp_adamw_tensor& t = tensors[i];
+    if (!std::isfinite(t.lr_mult) || !std::isfinite(t.weight_decay))
+      return fail(FP8MLP_ERR_INVALID_ARG, "lr_mult and weight_decay must be finite");
+    if (t.n == 0) continue;
+    float* p = t.p;
+    uint16_t* p_bf16 = t.p_bf16;
+    void *m = t.m, *v = t.v;
+    float *m_scale = t.m_scale, *v_scale = t.v_scale;
+    if (p == nullptr && p_bf16 == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "p and p_bf16 are both NULL");
+    if (p != nullptr) REQUIRE_PTR(p);
+    if (p_bf16 != nullptr) REQUIRE_PTR(p_bf16);
+    REQUIRE_PTR(m);
+    REQUIRE_PTR(v);
+    if (state_bits == 8) {
+      REQUIRE_PTR4(m_scale);
+      REQUIRE_PTR4(v_scale);
+    }
+  }
+  DeviceInfo* di = nullptr;
+  TRY(current_device(&di));
+  const cudaError_t e =
+      launch_adamw(n_tensors, tensors, st, state_bits, beta1, beta2, eps, grad_coef, di->status, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "adamw_step launch");
 }
 
 int fp8mlp_get_device_status(unsigned int* status, fp8mlp_stream_t stream) {

@@ -1,0 +1,385 @@
+// Warp-specialised, persistent tcgen05 GEMM on e4m3 operands with a scale for
+// each block of 128:
+//
+//   y[m, n] = sum_kb xs[kb, m] * ws[kb, n / 128] * sum_{k in kb} xq[m, k] Wq[n, k]
+//
+// The scales vary along K, so a sum over all of K cannot stay in TMEM.  One
+// pipeline stage is one 128-byte swizzle row of e4m3, which is one scale
+// block: its four UMMAs start a fresh TMEM accumulator, and the epilogue
+// warps add that partial sum, times xs * ws, to fp32 sums in registers while
+// the tensor cores fill the next accumulator (512 TMEM columns hold 512 / BN
+// of them).  A thread owns one row and 128 columns, i.e. one weight block: the
+// factor is one number per thread and k-block, and for the relu^2 output the
+// thread holds a whole 1 x 128 scale block, so its maximum needs no exchange.
+//   warp 0      TMA producer: A/B k-blocks into a STAGES-deep ring
+//   warp 1      allocates TMEM, issues the UMMAs from one thread
+//   warps 2..   4 * BN / 128 epilogue warps
+// CG = 2: the CTAs of a cluster pair share a 2-CTA UMMA over 256 rows, as in
+// gemm_sm100.cuh.  TMA zero-fills rows and columns past the edges and clips
+// the stores.
+#pragma once
+
+#include "gemm_sm100.cuh"
+
+namespace fp8mlp {
+
+struct alignas(64) BlockGemmParams {
+  CUtensorMap tmA, tmB;
+  CUtensorMap tmOut;   // bf16 output, 32 x 32 tiles
+  CUtensorMap tmOut2;  // relu^2: e4m3 copy, 32 x 32 tiles
+  int M, N, K;
+  int tiles_m, tiles_n;
+  int n_blocks;          // ceil(N / 128): row length of ws
+  const float* xs;       // [ceil(K / 128)][M]
+  const float* ws;       // [ceil(K / 128)][n_blocks]
+  float* post_s;         // relu^2: [n_blocks][M] inverse scales of the e4m3 copy
+  unsigned int* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
+};
+
+template <int CG_, int BN_, int STAGES_, bool RELU2_, int NSLOT_>
+struct BlockCfg {
+  static constexpr int CG = CG_;
+  static constexpr int BM = 128;
+  static constexpr int TILE_M = BM * CG;
+  static constexpr int BN = BN_;
+  static constexpr int B_ROWS = BN / CG;
+  static constexpr int STAGES = STAGES_;
+  static constexpr bool RELU2 = RELU2_;
+  static constexpr int NSLOT = NSLOT_;
+  static constexpr int BK = 128;
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int B_BYTES = B_ROWS * BK;
+  static constexpr int STAGE_TX = CG * (A_BYTES + B_BYTES);
+  static constexpr uint32_t IDESC = dev::instr_desc(dev::FMT_E4M3, dev::FMT_E4M3, false, false, TILE_M, BN);
+  static constexpr int NBUF = 512 / BN;  // TMEM accumulators
+  static constexpr int NEPI = 4 * BN / 128;
+  static constexpr int THREADS = 64 + 32 * NEPI;
+  static constexpr int OUT_BUF = 32 * 32 * 2;
+  static constexpr int SLOT = OUT_BUF + (RELU2 ? 32 * 32 : 0);
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * (A_BYTES + B_BYTES) + NSLOT * NEPI * SLOT + NUM_BARS * 8 + 16;
+  static_assert(CG == 1 || CG == 2, "CTA group");
+  static_assert(BN == 128 || BN == 256, "whole weight blocks per epilogue warp");
+  static_assert(B_ROWS % 8 == 0 && SMEM_BYTES <= 232448, "shared memory");
+};
+
+namespace dev {
+
+// max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Scale of a block of 128 whose largest magnitude is `amax`: s maps amax onto
+// 448 and is at most 2^120, so that 1/s stays a normal number; an all-zero
+// block takes s = 1.  A block that holds an infinity or NaN takes s = 1 and
+// stores 1/s = NaN, so that what is computed from it is NaN instead of a
+// saturated code that looks finite.
+__device__ __forceinline__ float block_scale(float amax, float* inv) {
+  if (!(amax <= 3.4028234664e38f)) {
+    *inv = __int_as_float(0x7fc00000);
+    return 1.f;
+  }
+  const float s = amax > 0.f ? fminf(__fdiv_rn(FP8MLP_E4M3_MAX, amax), 1.329227995784916e36f) : 1.f;
+  *inv = __fdiv_rn(1.f, s);
+  return s;
+}
+
+}  // namespace dev
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_constant__ BlockGemmParams p) {
+  using namespace dev;
+  constexpr int CG = C::CG;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + C::STAGES * C::A_BYTES;
+  uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::NSLOT * C::NEPI * C::SLOT);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + C::NBUF;
+  uint64_t* fin = tempty + C::NBUF;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = static_cast<int>(blockIdx.x) / CG;
+  const int nunits = static_cast<int>(gridDim.x) / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < C::NBUF; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], C::NEPI * CG);  // one arrival per epilogue warp of the pair
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(tmem_holder, 512);
+    tmem_relinquish<CG>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  const WaitCtx w{p.status, abort_flag, p.timeout_ns};
+  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int num_kb = (p.K + C::BK - 1) / C::BK;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0 && !(p.debug_flags & FP8MLP_DEBUG_STALL_PRODUCER)) {
+      tma_prefetch_desc(&p.tmA);
+      tma_prefetch_desc(&p.tmB);
+      uint32_t stage = 0, phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int t = unit; t < num_tiles && ok; t += nunits) {
+        const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+        const int m0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM;
+        const int n0 = nb * C::BN + static_cast<int>(rank) * C::B_ROWS;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = sA + stage * C::A_BYTES;
+          uint8_t* b = sB + stage * C::B_BYTES;
+          if constexpr (CG == 1) {
+            mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+            tma_load_2d(a, &p.tmA, &full[stage], kb * C::BK, m0);
+            tma_load_2d(b, &p.tmB, &full[stage], kb * C::BK, n0);
+          } else {
+            if (leader) mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            tma_load_2d_cg2(a, &p.tmA, fb, kb * C::BK, m0);
+            tma_load_2d_cg2(b, &p.tmB, fb, kb * C::BK, n0);
+          }
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the last copy into each stage must have landed before exit
+      if (leader) {
+        const long long n_drain = issued < C::STAGES ? issued : C::STAGES;
+        for (long long i = 0; i < n_drain; ++i) {
+          const long long n = issued - 1 - i;
+          mbar_wait_drain(&full[n % C::STAGES], static_cast<uint32_t>((n / C::STAGES) & 1), p.timeout_ns);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+      bool ok = true;
+      for (int t = unit; t < num_tiles && ok; t += nunits) {
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(&tempty[buf], buf_phase ^ 1u, w) || !mbar_wait(&full[stage], phase, w)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + stage * C::A_BYTES);
+          const uint32_t b0 = smem_u32(sB + stage * C::B_BYTES);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024), smem_desc(b0 + k * 32, 16, 1024),
+                           C::IDESC, k != 0 ? 1u : 0u);
+          if constexpr (CG == 1) {
+            tc_commit(&empty[stage]);
+            tc_commit(&tfull[buf]);
+          } else {
+            tc_commit_cg2_mc(&empty[stage], 0x3);
+            tc_commit_cg2_mc(&tfull[buf], 0x3);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == C::NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      // every UMMA this thread issued must be complete before TMEM is freed
+      if constexpr (CG == 1)
+        tc_commit(fin);
+      else
+        tc_commit_cg2(fin);
+      mbar_wait_drain(fin, 0, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quarter
+    const int e = warp - 2;
+    const int half = e / 4;  // which 128 columns of the tile
+    const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
+    uint32_t buf = 0, buf_phase = 0, ctr = 0;
+
+    // this thread's two scales of k-block kb of tile t; past the last k-block
+    // of a tile those of the next tile's first ones, so that they are under
+    // way while the current tile is written
+    auto scales = [&](int t, int kb, float& a, float& b) {
+      a = 0.f;
+      b = 0.f;
+      while (kb >= num_kb) {
+        kb -= num_kb;
+        t += nunits;
+      }
+      if (t >= num_tiles) return;
+      const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+      const int m = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32 + lane;
+      const int nblk = nb * (C::BN / 128) + half;
+      if (m < p.M) a = __ldg(p.xs + static_cast<size_t>(kb) * p.M + m);
+      if (nblk < p.n_blocks) b = __ldg(p.ws + static_cast<size_t>(kb) * p.n_blocks + nblk);
+    };
+    float a0 = 0.f, b0 = 0.f, a1 = 0.f, b1 = 0.f;
+    scales(unit, 0, a0, b0);
+    scales(unit, 1, a1, b1);
+
+    bool ok = true;
+    for (int t = unit; t < num_tiles; t += nunits) {
+      const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+      const int row0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32;
+      const int n0 = nb * C::BN + half * 128;
+      uint64_t acc[64];  // 128 fp32 sums as pairs
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        float a2, b2;
+        scales(t, kb + 2, a2, b2);
+        const float f = __fmul_rn(a0, b0);
+        const uint64_t f2 = f2_pack(f, f);
+        a0 = a1;
+        b0 = b1;
+        a1 = a2;
+        b1 = b2;
+        if (!mbar_wait(&tfull[buf], buf_phase, w)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tmem_mine + buf * C::BN + c * 32, v);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 1)
+                mbar_arrive(&tempty[buf]);
+              else
+                mbar_arrive_cluster(tempty0 + buf * 8u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] = f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2,
+                                     acc[c * 16 + i]);
+        }
+        if (++buf == C::NBUF) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      float s = 1.f;
+      if constexpr (C::RELU2) {
+        // post = relu(acc)^2 in place, its maximum over this 1 x 128 block
+        // (columns past N are zero), and the block's scale.  The codes are
+        // rounded once, from the fp32 value.
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          float u, v;
+          f2_unpack(acc[i], u, v);
+          u = max_nan(u, 0.f);
+          v = max_nan(v, 0.f);
+          u = __fmul_rn(u, u);
+          v = __fmul_rn(v, v);
+          amax = max_nan(amax, max_nan(u, v));
+          acc[i] = f2_pack(u, v);
+        }
+        float inv;
+        s = block_scale(amax, &inv);
+        if (row0 + lane < p.M && n0 < p.N) p.post_s[static_cast<size_t>(n0 >> 7) * p.M + row0 + lane] = inv;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint8_t* slot = sEpi + (e * C::NSLOT + (C::NSLOT == 2 ? (ctr & 1u) : 0u)) * C::SLOT;
+        const uint32_t sbase = smem_u32(slot);
+        if (lane == 0) bulk_wait_read<C::NSLOT - 1>();
+        __syncwarp();
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float u, v;
+          f2_unpack(acc[c * 16 + i], u, v);
+          pk[i] = pack_bf16x2(u, v);
+        }
+        store_row_bf16<64>(sbase, lane, pk);
+        if constexpr (C::RELU2) {
+          uint32_t qk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float u0, u1, u2, u3;
+            f2_unpack(acc[c * 16 + 2 * i], u0, u1);
+            f2_unpack(acc[c * 16 + 2 * i + 1], u2, u3);
+            qk[i] = pack_e4m3x2(__fmul_rn(u0, s), __fmul_rn(u1, s)) |
+                    (pack_e4m3x2(__fmul_rn(u2, s), __fmul_rn(u3, s)) << 16);
+          }
+          const uint32_t qb = sbase + C::OUT_BUF;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            st_shared_v4(qb + swz<1>(lane * 32 + j * 16), qk[4 * j], qk[4 * j + 1], qk[4 * j + 2], qk[4 * j + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&p.tmOut, slot, n0 + c * 32, row0);
+          if constexpr (C::RELU2) tma_store_2d(&p.tmOut2, slot + C::OUT_BUF, n0 + c * 32, row0);
+          bulk_commit();
+        }
+        ++ctr;
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem_base, 512);
+  }
+}
+
+}  // namespace fp8mlp

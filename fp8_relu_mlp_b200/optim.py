@@ -1,0 +1,96 @@
+"""AdamW over a model's tensors: buffers and the two library calls of a step.
+
+One step is the norm of all gradients with the clip coefficient
+(``fp8mlp_grad_norm``, when ``max_norm`` is given) and one pass over all
+tensors (``fp8mlp_adamw_step``): every weight, its BF16 copy, gradient and
+moments are read and written once.  Moments are fp32 or, with
+``state_bits=8``, e4m3 codes with a scale for each block of 128 (2.06 bytes
+per element in place of 8).  Nothing is read back to the host, so a step can
+be captured into a CUDA graph; lr, the step count and the seed live on the
+device.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _abi as A
+
+
+class AdamW:
+    def __init__(self, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8, seed: int = 0,
+                 max_norm: float | None = None, step_count: int = 0, device="cuda", stream=None):
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be > 0")
+        if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1 and eps > 0):
+            raise ValueError("betas must be in [0, 1) and eps > 0")
+        self.state_bits, self.betas, self.eps, self.max_norm = state_bits, tuple(betas), eps, max_norm
+        self.device, self.stream = torch.device(device), stream
+        self.entries = []  # the tensors of each parameter: the descriptors hold their addresses
+        self._descriptors = []
+        self._plan = self._workspace = None
+        self.state = torch.zeros(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
+        self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
+        A.fp8mlp_adamw_state_init(self.state, lr, seed & 0xFFFFFFFF, step_count, stream)
+
+    def add(self, grad, master=None, weight=None, weight_decay: float = 0.0, lr_mult: float = 1.0, state=None) -> dict:
+        """One parameter: ``grad`` fp32; ``master`` fp32 weights and / or
+        ``weight`` the BF16 weights (a copy where there is a master, else the
+        weights themselves, rounded stochastically).  ``state`` may bring the
+        moments (``m``, ``v`` and with 8 bits ``m_scale``, ``v_scale``); else
+        they are allocated and start at zero.  Returns the entry."""
+        n = grad.numel()
+        if grad.dtype != torch.float32:
+            raise ValueError("grad must be fp32")
+        if master is None and weight is None:
+            raise ValueError("master or weight is needed")
+        if master is not None and (master.dtype != torch.float32 or master.numel() != n):
+            raise ValueError("master must be fp32 of the gradient's size")
+        if weight is not None and (weight.dtype != torch.bfloat16 or weight.numel() != n):
+            raise ValueError("weight must be bf16 of the gradient's size")
+        if state is None:
+            if self.state_bits == 32:
+                state = {k: torch.zeros(n, dtype=torch.float32, device=grad.device) for k in ("m", "v")}
+            else:
+                state = {k: torch.zeros(n, dtype=torch.float8_e4m3fn, device=grad.device) for k in ("m", "v")}
+                state.update({k: torch.ones(-(-n // 128), dtype=torch.float32, device=grad.device)
+                              for k in ("m_scale", "v_scale")})
+        size = self.state_bits // 8
+        if state["m"].element_size() != size or state["v"].element_size() != size:
+            raise ValueError(f"the moments must have {self.state_bits} bits")
+        if self.state_bits == 8 and not ("m_scale" in state and "v_scale" in state):
+            raise ValueError("8-bit moments need m_scale and v_scale")
+        e = dict(grad=grad, master=master, weight=weight, **state)
+        new = {t.data_ptr() for t in e.values() if t is not None and t.numel()}
+        if len(new) < sum(t is not None and t.numel() > 0 for t in e.values()) or new & {
+                t.data_ptr() for o in self.entries for t in o.values() if t is not None}:
+            raise ValueError("a tensor is given twice: one step updates each weight once")
+        self._descriptors.append(A.adamw_tensor(
+            n, master, weight, grad, state["m"], state["v"], state.get("m_scale"), state.get("v_scale"), lr_mult,
+            weight_decay, self.state_bits))
+        self.entries.append(e)
+        self._plan = None
+        return e
+
+    def set_lr(self, lr: float):
+        """For the steps from here on (a device write; also between replays of
+        a captured step)."""
+        self.state[:1].view(torch.float32).fill_(lr)
+
+    def step(self):
+        if self._plan is None:
+            self._plan = A.adamw_tensors(self._descriptors)
+            if self.max_norm is not None:
+                self._workspace = torch.empty(A.fp8mlp_grad_norm_workspace_size(self._plan), dtype=torch.uint8,
+                                              device=self.device)
+        coef = None
+        if self.max_norm is not None:
+            A.fp8mlp_grad_norm(self._plan, self.max_norm, self.norm, self._workspace, self.stream)
+            coef = self.norm[1:]
+        A.fp8mlp_adamw_step(self._plan, self.state, self.state_bits, *self.betas, self.eps, coef, self.stream)
+
+    def read_state(self) -> dict:
+        s = self.state.cpu()
+        return dict(lr=float(s.view(torch.float32)[0]), step=int(s[1]), seed=int(s[2]) & 0xFFFFFFFF,
+                    skipped=int(s[4]))

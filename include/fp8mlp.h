@@ -77,6 +77,7 @@ typedef struct CUstream_st* fp8mlp_stream_t; /* same type as cudaStream_t */
 #define FP8MLP_STATUS_TIMEOUT 1u          /* a kernel's bounded wait gave up */
 #define FP8MLP_STATUS_NONFINITE_AMAX 2u   /* amax was NaN/inf: scale kept */
 #define FP8MLP_STATUS_W2_DEGENERATE 4u    /* max|W2| was 0 or not finite: s_w = 1 */
+#define FP8MLP_STATUS_STEP_SKIPPED 8u     /* an AdamW step saw a coefficient that is not finite */
 
 /* Largest finite e4m3 value; the delayed scale maps margin * amax onto it. */
 #define FP8MLP_E4M3_MAX 448.0f
@@ -475,6 +476,165 @@ int fp8mlp_rmsnorm_bwd(int M, int d, const uint16_t* r, const float* rstd, const
 /* r_next = bf16(r + out), [M,d]. */
 int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, uint16_t* r_next,
                         fp8mlp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 products with a scale for each block of 128 (no delayed scale, no
+ * calibration step).  Activations take one scale per row and group of 128
+ * along the contraction, weights one per 128 x 128 block:
+ *   s    = min(fp32(448 / amax), 2^120), 1 for an all-zero block
+ *   code = e4m3_satfinite(fp32(value * s)),  stored scale = fp32(1 / s)
+ * A block that holds an infinity or NaN takes s = 1 and stores NaN, so what
+ * is computed from it is NaN.  Scales are fp32, block of the contraction
+ * outermost: xs [ceil(K/128)][M], ws [ceil(K/128)][ceil(N/128)].  The last
+ * group and the last weight blocks may be shorter.  4-byte alignment is
+ * enough for the scales.
+ *   y[m,n] = bf16( sum_b fp32(xs[b,m] ws[b,n/128]) sum_{k in b} xq[m,k] Wq[n,k] )
+ * with fp32 sums.  The gradient with respect to x is the same product over
+ * the transposed cache, fp8mlp_linear_block(M, N, K, dY, Wq_t, ws_t, ...);
+ * the weight gradient stays BF16 (fp8mlp_linear_bwd).
+ * ------------------------------------------------------------------------ */
+
+/* x [M,K] bf16 -> xq [M,K] e4m3, xs [ceil(K/128)][M] fp32. */
+int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, fp8mlp_stream_t stream);
+
+/* W [N,K] bf16 -> Wq [N,K] e4m3 with ws [ceil(K/128)][ceil(N/128)], and / or
+ * the transposed Wq_t [K,N] with ws_t [ceil(N/128)][ceil(K/128)] (the same
+ * codes and scales).  Either pair may be NULL, not both.  N, K <= 2^22. */
+int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t,
+                                      float* ws_t, fp8mlp_stream_t stream);
+
+/* y = the product above, from codes. */
+int fp8mlp_linear_fwd_block(int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
+                            const float* ws, uint16_t* y, fp8mlp_stream_t stream);
+
+/* The layer from BF16 activations: fp8mlp_quantize_block (xq and xs are
+ * written), then fp8mlp_linear_fwd_block. */
+int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* Wq, const float* ws, uint8_t* xq,
+                        float* xs, uint16_t* y, fp8mlp_stream_t stream);
+
+/* Up-projection of the ReLU^2 block: with acc the fp32 product of x and W1,
+ *   post = bf16(relu(acc)^2)  [M,h]   (for the BF16 backward, fp8mlp_mlp_bwd)
+ *   post_q, post_s = relu(acc)^2 quantised along h, rounded once from fp32;
+ *                    post_s [ceil(h/128)][M]
+ * W1q [h,d], w1s [ceil(d/128)][ceil(h/128)].  A NaN in acc stays NaN. */
+int fp8mlp_up_proj_block(int M, int d, int h, const uint8_t* xq, const float* xs, const uint8_t* W1q,
+                         const float* w1s, uint16_t* post, uint8_t* post_q, float* post_s, fp8mlp_stream_t stream);
+
+/* The whole MLP forward from BF16 x: quantise x, fp8mlp_up_proj_block, and
+ * the down-projection out = fp8mlp_linear_fwd_block(M, h, d, post_q, post_s,
+ * W2q_t, w2s_t) with W2q_t [d,h] and w2s_t [ceil(h/128)][ceil(d/128)], the
+ * transposed cache of W2 [h,d]. */
+int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* W1q, const float* w1s,
+                         const uint8_t* W2q_t, const float* w2s_t, uint8_t* xq, float* xs, uint16_t* post,
+                         uint8_t* post_q, float* post_s, uint16_t* out, fp8mlp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms after one block and before the next, fused with the gate and the
+ * residual scale:
+ *   n = y rstd_post            rstd_post[m] = 1 / sqrt(mean(y[m,:]^2) + eps)
+ *   r' = alpha r + gate (n w_post)
+ *   x  = r' rstd_pre w_pre     rstd_pre[m]  = 1 / sqrt(mean(r'[m,:]^2) + eps)
+ * r, y, r_next (= r'), x [M,d] bf16; w_post, w_pre [d] bf16; gate
+ * [ceil(M / rows_per_gate)][d] bf16, row m takes gate row m / rows_per_gate
+ * (rows_per_gate >= M: one gate for all rows, 1: a gate per row); alpha one
+ * fp32 on the device; rstd_* [M] fp32.  All arithmetic is fp32 and each
+ * output is rounded once: x is computed from r' before r' is rounded.
+ * NULL for w_post, w_pre, gate or alpha means 1.  y = NULL leaves out the
+ * first part (then w_post, gate, alpha, r_next and rstd_post are NULL, and
+ * x = norm(r) w_pre); x = NULL leaves out the second (then w_pre, rstd_pre, xq
+ * and xs are NULL); not both.  xq, xs (both or neither): x quantised
+ * as by fp8mlp_quantize_block, rounded once from fp32.  r_next may equal r, x may
+ * equal y.  d <= 8192.  eps finite and > 0.
+ * ------------------------------------------------------------------------ */
+int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
+                         const uint16_t* gate, int rows_per_gate, const float* alpha, const uint16_t* w_pre, float eps,
+                         uint16_t* r_next, float* rstd_post, uint16_t* x, float* rstd_pre, uint8_t* xq, float* xs,
+                         fp8mlp_stream_t stream);
+
+/* Gradient, from dx = dL/dx and dr_next = dL/dr' (NULL: 0), both [M,d] bf16:
+ *   D  = dr_next + rstd_pre (w_pre dx - xh mean(w_pre dx xh)),   xh = r' rstd_pre
+ *   dr = bf16(alpha D)
+ *   dy = bf16(rstd_post (D gate w_post - n mean(D gate w_post n)))
+ *   dw_post[j] = sum_m D gate n   dw_pre[j] = sum_m dx xh     (fp32 [d])
+ *   dgate[i,j] = sum over gate row i's rows of D n w_post     (fp32, gate's shape)
+ *   dalpha = sum D r                                          (fp32)
+ * y, dx and what belongs to them are NULL as in the forward (with y = NULL,
+ * r_next is r and dr = D).  Any of dw_post, dgate, dalpha, dw_pre may be NULL;
+ * r is read for dalpha only.  dr may equal dr_next, dy may equal y or dx.  The sums are taken
+ * in a fixed order.  M = 0 zeroes dw_post, dw_pre and dalpha.
+ * workspace: fp8mlp_norm_gate_bwd_workspace_size bytes, no initial contents;
+ * calls that may overlap on the GPU need workspaces of their own. */
+int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
+                         const uint16_t* gate, int rows_per_gate, const float* alpha, const float* rstd_post,
+                         const uint16_t* r_next, const uint16_t* w_pre, const float* rstd_pre, const uint16_t* dx,
+                         const uint16_t* dr_next, uint16_t* dr, uint16_t* dy, float* dw_post, float* dgate,
+                         float* dalpha, float* dw_pre, void* workspace, fp8mlp_stream_t stream);
+size_t fp8mlp_norm_gate_bwd_workspace_size(int M, int d, int rows_per_gate);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors at once
+ *   g' = coef g        m' = b1 m + (1 - b1) g'       v' = b2 v + (1 - b2) g'^2
+ *   p' = p - lr wd p - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+ * every product and sum rounded to fp32.
+ * ------------------------------------------------------------------------ */
+
+/* One tensor of n >= 0 elements, its arrays dense and 16-byte aligned:
+ *   p       fp32 weights (read and written), or NULL
+ *   p_bf16  bf16 weights: with p a copy that is written (or NULL); without p
+ *           the weights themselves, then rounded stochastically
+ *   g       fp32 gradient
+ *   m, v    state_bits 32: fp32 [n].  state_bits 8: e4m3 codes [n] of m and
+ *           of sqrt(v), with fp32 scales m_scale, v_scale [ceil(n/128)] (value
+ *           = code * scale; scales as in fp8mlp_quantize_block); codes are
+ *           rounded stochastically, and a positive sqrt(v) keeps at least
+ *           the smallest code.  Zero codes with any finite scale start a state.
+ *   lr_mult, weight_decay: the tensor's own factor of lr, and wd
+ * No array may overlap another one of the call. */
+typedef struct fp8mlp_adamw_tensor {
+  int64_t n;
+  float* p;
+  uint16_t* p_bf16;
+  const float* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float lr_mult;
+  float weight_decay;
+} fp8mlp_adamw_tensor;
+
+/* Device-resident, caller-allocated (32 bytes, 16-byte aligned).  A step reads
+ * lr and seed and advances step, so captured steps can be replayed; lr may be
+ * written between steps.  May be copied out and back in. */
+typedef struct fp8mlp_adamw_state {
+  float lr;
+  int32_t step;     /* steps taken */
+  uint32_t seed;    /* of the stochastic rounding */
+  uint32_t arrived; /* the step's own, 0 between steps */
+  int32_t skipped;  /* steps not taken (coefficient not finite) */
+  int32_t pad[3];
+} fp8mlp_adamw_state;
+
+/* lr finite, step >= 0. */
+int fp8mlp_adamw_state_init(fp8mlp_adamw_state* st, float lr, uint32_t seed, int step, fp8mlp_stream_t stream);
+
+/* norm_coef[0] = the 2-norm over all gradients (sums in double),
+ * norm_coef[1] = min(1, max_norm / (norm + 1e-6)), NaN if the norm is not
+ * finite.  Reads n and g of each tensor.  max_norm > 0 (may be infinite).
+ * workspace: fp8mlp_grad_norm_workspace_size bytes, 16-byte aligned, no
+ * initial contents; calls that may overlap need workspaces of their own. */
+int fp8mlp_grad_norm(int n_tensors, const fp8mlp_adamw_tensor* tensors, float max_norm, float* norm_coef,
+                     void* workspace, fp8mlp_stream_t stream);
+size_t fp8mlp_grad_norm_workspace_size(int n_tensors, const fp8mlp_adamw_tensor* tensors);
+
+/* One step of all tensors (`tensors`: HOST array, read before the call
+ * returns).  grad_coef: device fp32 or NULL (1); where it is NaN or infinite
+ * nothing but st->skipped changes and FP8MLP_STATUS_STEP_SKIPPED is set.
+ * state_bits 32 or 8.  0 <= beta < 1, eps > 0.  Random bits are a function of
+ * st->seed, the step, the tensor's place in the call and the element's index.
+ * Steps that share st run one after another. */
+int fp8mlp_adamw_step(int n_tensors, const fp8mlp_adamw_tensor* tensors, fp8mlp_adamw_state* st, int state_bits,
+                      float beta1, float beta2, float eps, const float* grad_coef, fp8mlp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Status and diagnostics

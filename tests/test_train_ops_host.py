@@ -1,0 +1,190 @@
+"""Host-side refusals of the block-scaled products, the gated norms and the
+optimizer (no GPU needed: arguments are checked before any CUDA call), the
+descriptor's layout, and the plain definitions against differences."""
+import ctypes
+import re
+
+import pytest
+import torch
+
+from fp8_relu_mlp_b200 import _abi as A
+import train_ops_ref as R
+
+F = 0x10000  # 16-byte aligned, never dereferenced on the host
+INVALID, SHAPE = A.ERR_INVALID_ARG, A.ERR_UNSUPPORTED_SHAPE
+
+
+def refused(code, fn, *args):
+    with pytest.raises(A.Fp8MlpError) as e:
+        fn(*args, stream=0)
+    assert e.value.code == code, str(e.value)
+
+
+BLOCK_CALLS = {
+    "linear_fwd_block": (A.fp8mlp_linear_fwd_block, [4, 128, 256], [F] * 5),
+    "linear_block": (A.fp8mlp_linear_block, [4, 128, 256], [F] * 6),
+    "up_proj_block": (A.fp8mlp_up_proj_block, [4, 128, 256], [F] * 7),
+    "mlp_fwd_block": (A.fp8mlp_mlp_fwd_block, [4, 128, 256], [F] * 11),
+    "quantize_block": (A.fp8mlp_quantize_block, [4, 128], [F] * 3),
+}
+
+
+@pytest.mark.parametrize("name", BLOCK_CALLS)
+def test_block_products_refuse(name):
+    fn, sizes, ptrs = BLOCK_CALLS[name]
+    refused(INVALID, fn, -1, *sizes[1:], *ptrs)
+    for i in range(1, len(sizes)):
+        for bad in (0, 8, 24, -16):
+            refused(SHAPE, fn, *[bad if k == i else v for k, v in enumerate(sizes)], *ptrs)
+    for i in range(len(ptrs)):
+        refused(INVALID, fn, *sizes, *[None if k == i else v for k, v in enumerate(ptrs)])
+        refused(INVALID, fn, *sizes, *[F + 2 if k == i else v for k, v in enumerate(ptrs)])
+    # an empty batch is no error and touches nothing
+    assert fn(0, *sizes[1:], *[None] * len(ptrs), stream=0) == A.OK
+    if not torch.cuda.is_available():
+        refused(A.ERR_NO_DEVICE, fn, *sizes, *ptrs)
+
+
+def test_weight_cache_refuses():
+    f = A.fp8mlp_weight_block_cache_refresh
+    refused(SHAPE, f, 24, 16, F, F, F, F, F)
+    refused(SHAPE, f, (1 << 22) + 16, 16, F, F, F, F, F)
+    refused(INVALID, f, 16, 16, None, F, F, F, F)
+    refused(INVALID, f, 16, 16, F, None, None, None, None)
+    refused(INVALID, f, 16, 16, F, F, None, None, None)
+    refused(INVALID, f, 16, 16, F, F, F, F, None)
+    refused(INVALID, f, 16, 16, F, F + 8, F, None, None)
+
+
+FWD = dict(M=4, d=64, r=F, y=F, w_post=F, gate=F, rows_per_gate=2, alpha=F, w_pre=F, eps=1e-6, r_next=F, rstd_post=F, x=F,
+           rstd_pre=F, xq=F, xs=F)
+BWD = dict(M=4, d=64, r=F, y=F, w_post=F, gate=F, rows_per_gate=2, alpha=F, rstd_post=F, r_next=F, w_pre=F, rstd_pre=F, dx=F,
+           dr_next=F, dr=F, dy=F, dw_post=F, dgate=F, dalpha=F, dw_pre=F, workspace=F)
+
+
+@pytest.mark.parametrize("code,change", [
+    (INVALID, dict(M=-1)), (SHAPE, dict(d=24)), (SHAPE, dict(d=8208)), (INVALID, dict(rows_per_gate=0)),
+    (INVALID, dict(eps=0.0)), (INVALID, dict(eps=float("nan"))), (INVALID, dict(eps=float("inf"))), (INVALID, dict(r=None)),
+    (INVALID, dict(xq=None)), (INVALID, dict(xs=None)), (INVALID, dict(r_next=None)), (INVALID, dict(rstd_post=None)),
+    (INVALID, dict(rstd_pre=None)), (INVALID, dict(y=None)), (INVALID, dict(x=None)), (INVALID, dict(r=F + 8)),
+    (INVALID, dict(gate=F + 4)), (INVALID, dict(alpha=F + 2)), (INVALID, dict(xq=F + 4)), (INVALID, dict(w_pre=F + 2)),
+    (INVALID, dict(y=None, w_post=None, gate=None, alpha=None, r_next=None, rstd_post=None, x=None, w_pre=None,
+                   rstd_pre=None, xq=None, xs=None))])
+def test_norms_refuse(code, change):
+    refused(code, A.fp8mlp_norm_gate_fwd, *dict(FWD, **change).values())
+
+
+@pytest.mark.parametrize("code,change", [
+    (INVALID, dict(M=-1)), (SHAPE, dict(d=8)), (SHAPE, dict(d=8208)), (INVALID, dict(rows_per_gate=-3)),
+    (INVALID, dict(r=None)), (INVALID, dict(y=None)), (INVALID, dict(dx=None)), (INVALID, dict(dr=None)),
+    (INVALID, dict(dy=None)), (INVALID, dict(rstd_post=None)), (INVALID, dict(rstd_pre=None)), (INVALID, dict(r_next=None)),
+    (INVALID, dict(workspace=None)), (INVALID, dict(workspace=F + 8)), (INVALID, dict(dgate=F + 4)),
+    (INVALID, dict(dr_next=F + 2)), (INVALID, dict(dalpha=F + 1))])
+def test_norm_gradients_refuse(code, change):
+    refused(code, A.fp8mlp_norm_gate_bwd, *dict(BWD, **change).values())
+
+
+@pytest.mark.parametrize("M,d,rows", [(1, 16, 1), (16384, 768, 16384), (5000, 1040, 7), (3, 8192, 1)])
+def test_norm_workspace_covers_the_parts(M, d, rows):
+    need = A.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows)
+    assert need >= 2 * 4 * d + 8 and need <= 8 * 4 * d * 2400
+    assert A.fp8mlp_norm_gate_bwd_workspace_size(0, d, rows) == 0
+    assert A.fp8mlp_norm_gate_bwd_workspace_size(M, d, 0) == 0
+
+
+def tensor(**kw):
+    d = dict(n=10, p=F, p_bf16=F, g=F, m=F, v=F, m_scale=F, v_scale=F, lr_mult=1.0, weight_decay=0.0)
+    return A.adamw_tensors([A.AdamwTensor(*dict(d, **kw).values())])
+
+
+@pytest.mark.parametrize("code,change", [
+    (INVALID, dict(n=-1)), (SHAPE, dict(n=(1 << 42) + 1)), (SHAPE, dict(n=1 << 42, )), (INVALID, dict(g=None)),
+    (INVALID, dict(g=F + 4)), (INVALID, dict(p=None, p_bf16=None)), (INVALID, dict(p=F + 8)), (INVALID, dict(p_bf16=F + 2)),
+    (INVALID, dict(m=None)), (INVALID, dict(v=None)), (INVALID, dict(m_scale=None)), (INVALID, dict(v_scale=F + 1)),
+    (INVALID, dict(lr_mult=float("nan"))), (INVALID, dict(weight_decay=float("inf")))])
+def test_adamw_refuses_tensors(code, change):
+    if change == dict(n=1 << 42):
+        arr = A.adamw_tensors([tensor(**change)[0], tensor(**change)[0], tensor(n=1 << 41)[0]] + [tensor(**change)[0]] * 2)
+    else:
+        arr = tensor(**change)
+    refused(code, A.fp8mlp_adamw_step, arr, F, 8, 0.9, 0.95, 1e-8, F)
+
+
+@pytest.mark.parametrize("args", [(F, 16, 0.9, 0.95, 1e-8, None), (None, 8, 0.9, 0.95, 1e-8, None),
+                                  (F, 8, 1.0, 0.95, 1e-8, None), (F, 8, 0.9, -0.1, 1e-8, None),
+                                  (F, 8, 0.9, float("nan"), 1e-8, None), (F, 8, 0.9, 0.95, 0.0, None),
+                                  (F, 8, 0.9, 0.95, 1e-8, F + 2), (F + 8, 8, 0.9, 0.95, 1e-8, None)])
+def test_adamw_refuses_scalars(args):
+    refused(INVALID, A.fp8mlp_adamw_step, tensor(), *args)
+
+
+def test_optimizer_helpers_refuse():
+    refused(INVALID, A.fp8mlp_grad_norm, tensor(), 0.0, F, F)
+    refused(INVALID, A.fp8mlp_grad_norm, tensor(), float("nan"), F, F)
+    refused(INVALID, A.fp8mlp_grad_norm, tensor(), 1.0, None, F)
+    refused(INVALID, A.fp8mlp_grad_norm, tensor(), 1.0, F, None)
+    refused(INVALID, A.fp8mlp_grad_norm, tensor(n=-2), 1.0, F, F)
+    refused(INVALID, A.fp8mlp_adamw_state_init, F, float("inf"), 0, 0)
+    refused(INVALID, A.fp8mlp_adamw_state_init, F, 1e-3, 0, -1)
+    with pytest.raises(TypeError):
+        A.fp8mlp_adamw_step([], F, 8, 0.9, 0.95, 1e-8)
+    with pytest.raises(ValueError, match="CUDA"):
+        A.adamw_tensor(4, torch.zeros(4), None, torch.zeros(4), torch.zeros(4), torch.zeros(4))
+    # scales are not asked for with 32-bit states
+    if not torch.cuda.is_available():
+        refused(A.ERR_NO_DEVICE, A.fp8mlp_adamw_step, tensor(m_scale=None, v_scale=None), F, 32, 0.9, 0.95, 1e-8, None)
+    assert A.fp8mlp_grad_norm_workspace_size(tensor(n=16385)) == 16
+    assert A.fp8mlp_grad_norm_workspace_size(A.adamw_tensors([])) == 16
+    assert A.fp8mlp_grad_norm_workspace_size(tensor(n=16384 * 5 + 1)) == 48
+
+
+def test_struct_layouts():
+    text = open(A.HEADER).read()
+    body = re.search(r"typedef struct fp8mlp_adamw_state \{(.*?)\} fp8mlp_adamw_state;", text, re.S).group(1)
+    fields = re.findall(r"(?:float|int32_t|uint32_t)\s+\w+(?:\[(\d+)\])?;", body)
+    assert sum(4 * int(f or 1) for f in fields) == 32
+    body = re.search(r"typedef struct fp8mlp_adamw_tensor \{(.*?)\} fp8mlp_adamw_tensor;", text, re.S).group(1)
+    names = re.findall(r"(\w+);", body)
+    assert names == [f[0] for f in A.AdamwTensor._fields_] and ctypes.sizeof(A.AdamwTensor) == 72
+
+
+def test_the_plain_norm_gradient_agrees_with_differences():
+    torch.manual_seed(0)
+    M, d, rows = 7, 32, 3
+    t = lambda *s: torch.randn(*s, dtype=R.F64)  # noqa: E731
+    q = dict(r=t(M, d), y=t(M, d), w_post=t(d), gate=t(3, d), alpha=t(1), w_pre=t(d))
+    cx, cr = t(M, d), t(M, d)
+
+    def loss(q):
+        rn, _, x, _ = R.norms_fwd(q["r"], q["y"], q["w_post"], q["gate"], rows, q["alpha"], q["w_pre"], 1e-6)
+        return float((x * cx).sum() + (rn * cr).sum())
+
+    rn, rpost, _, rpre = R.norms_fwd(q["r"], q["y"], q["w_post"], q["gate"], rows, q["alpha"], q["w_pre"], 1e-6)
+    out, _ = R.norms_bwd(q["r"], q["y"], q["w_post"], q["gate"], rows, q["alpha"], rpost, rn, q["w_pre"], rpre, cx, cr)
+    for k, g in dict(r="dr", y="dy", w_post="dw_post", gate="dgate", alpha="dalpha", w_pre="dw_pre").items():
+        v = torch.randn_like(q[k])
+        num = (loss({**q, k: q[k] + 1e-6 * v}) - loss({**q, k: q[k] - 1e-6 * v})) / 2e-6
+        assert abs(num - float((out[g] * v).sum())) < 1e-5 * (1 + abs(num)), k
+
+
+def test_the_plain_step_agrees_with_float64():
+    torch.manual_seed(1)
+    n = 500
+    p, g, m, v = torch.randn(n) * 0.02, torch.randn(n) * 1e-3, torch.randn(n) * 1e-3, torch.rand(n) * 1e-6
+    a = R.adamw(p, g, m, v, 7, 1e-3, 0.1, 0.9, 0.95, 1e-8)
+    b = R.adamw64(p, g, m, v, 7, 1e-3, 0.1, 0.9, 0.95, 1e-8)
+    for x, y in zip(a, b):
+        assert float((x.double() - y).abs().max()) <= 2.0 ** -20 * float(y.abs().max())
+
+
+def test_stochastic_rounding_of_the_plain_form():
+    # between two codes with the right frequency, never beyond them, exact codes kept
+    n = 1 << 16
+    u = torch.arange(n).float() / n
+    for x, lo, hi in [(100.0, 96.0, 104.0), (1.03, 1.0, 1.125), (0.003, 2.0 ** -9, 2.0 ** -8), (448.0, 448.0, 448.0)]:
+        t = torch.full((n,), x)
+        t[::128] = 448.0  # every block's scale is 1
+        q, s = R.quant_state(t, u, False)
+        assert bool((s == 1).all())
+        rest = q[torch.arange(n) % 128 != 0]
+        assert set(rest.tolist()) <= {lo, hi} and abs(float(rest.mean()) - x) < 1e-3 * x + 2e-5
