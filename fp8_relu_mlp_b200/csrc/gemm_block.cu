@@ -26,6 +26,13 @@ cudaError_t launch_cfg(BlockGemmParams& p, int num_sms, cudaStream_t s) {
   if (dev < 0 || dev >= kMaxDevices || !attr_done[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(gemm_block_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
+    if (C::SPLIT_REGS) {
+      // the epilogue's larger share has to be there to be taken, or it would wait for good
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, gemm_block_kernel<C>);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs * C::THREADS < C::REGS_SUM) return cudaErrorLaunchOutOfResources;
+    }
     if (dev >= 0 && dev < kMaxDevices) attr_done[dev].store(true, std::memory_order_release);
   }
   p.tiles_m = (p.M + C::TILE_M - 1) / C::TILE_M;

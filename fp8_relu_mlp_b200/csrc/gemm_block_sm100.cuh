@@ -13,7 +13,7 @@
 // thread holds a whole 1 x 128 scale block, so its maximum needs no exchange.
 //   warp 0      TMA producer: A/B k-blocks into a STAGES-deep ring
 //   warp 1      allocates TMEM, issues the UMMAs from one thread
-//   warps 2..   4 * BN / 128 epilogue warps
+//   then        4 * BN / 128 epilogue warps (from warp 2, or 4 with 8 of them)
 // CG = 2: the CTAs of a cluster pair share a 2-CTA UMMA over 256 rows, as in
 // gemm_sm100.cuh.  TMA zero-fills rows and columns past the edges and clips
 // the stores.
@@ -55,7 +55,13 @@ struct BlockCfg {
   static constexpr uint32_t IDESC = dev::instr_desc(dev::FMT_E4M3, dev::FMT_E4M3, false, false, TILE_M, BN);
   static constexpr int NBUF = 512 / BN;  // TMEM accumulators
   static constexpr int NEPI = 4 * BN / 128;
-  static constexpr int THREADS = 64 + 32 * NEPI;
+  // With eight epilogue warps a thread needs more than 65536 / 384 registers:
+  // the first warpgroup (producer, issuer, two idle warps) hands some over.
+  static constexpr bool SPLIT_REGS = NEPI == 8;
+  static constexpr int EPI0 = SPLIT_REGS ? 4 : 2;  // first epilogue warp
+  static constexpr int THREADS = 32 * (EPI0 + NEPI);
+  static constexpr int REGS_CONTROL = 56, REGS_EPI = 224;
+  static constexpr int REGS_SUM = 128 * REGS_CONTROL + 256 * REGS_EPI;  // of the launch, at least
   static constexpr int OUT_BUF = 32 * 32 * 2;
   static constexpr int SLOT = OUT_BUF + (RELU2 ? 32 * 32 : 0);
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
@@ -67,6 +73,15 @@ struct BlockCfg {
 };
 
 namespace dev {
+
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // max that keeps NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -144,6 +159,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   const int num_tiles = p.tiles_m * p.tiles_n;
   const int num_kb = (p.K + C::BK - 1) / C::BK;
 
+  if (warp < C::EPI0) {
+  if constexpr (C::SPLIT_REGS) reg_dec<C::REGS_CONTROL>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0 && !(p.debug_flags & FP8MLP_DEBUG_STALL_PRODUCER)) {
@@ -231,35 +248,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         tc_commit_cg2(fin);
       mbar_wait_drain(fin, 0, p.timeout_ns);
     }
+  }
   } else {
     // ------------------------------------------------------------ epilogue
+    if constexpr (C::SPLIT_REGS) reg_inc<C::REGS_EPI>();
     const int q = warp & 3;  // TMEM lane quarter
-    const int e = warp - 2;
+    const int e = warp - C::EPI0;
     const int half = e / 4;  // which 128 columns of the tile
     const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
     uint32_t buf = 0, buf_phase = 0, ctr = 0;
 
-    // this thread's two scales of k-block kb of tile t; past the last k-block
-    // of a tile those of the next tile's first ones, so that they are under
-    // way while the current tile is written
-    auto scales = [&](int t, int kb, float& a, float& b) {
-      a = 0.f;
-      b = 0.f;
-      while (kb >= num_kb) {
-        kb -= num_kb;
-        t += nunits;
-      }
-      if (t >= num_tiles) return;
-      const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+    // This thread's two scales, read two k-blocks ahead and across tiles: the
+    // next tile's first ones are under way while the current one is written.
+    int st = unit, skb = 0;
+    const float *px = nullptr, *pw = nullptr;
+    auto seek = [&]() {
+      px = pw = nullptr;
+      if (st >= num_tiles) return;
+      const int mb = st / p.tiles_n, nb = st - mb * p.tiles_n;
       const int m = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32 + lane;
       const int nblk = nb * (C::BN / 128) + half;
-      if (m < p.M) a = __ldg(p.xs + static_cast<size_t>(kb) * p.M + m);
-      if (nblk < p.n_blocks) b = __ldg(p.ws + static_cast<size_t>(kb) * p.n_blocks + nblk);
+      if (m < p.M) px = p.xs + m;
+      if (nblk < p.n_blocks) pw = p.ws + nblk;
     };
-    float a0 = 0.f, b0 = 0.f, a1 = 0.f, b1 = 0.f;
-    scales(unit, 0, a0, b0);
-    scales(unit, 1, a1, b1);
+    auto scales = [&](float& a, float& b) {
+      a = px != nullptr ? __ldg(px + static_cast<size_t>(skb) * p.M) : 0.f;
+      b = pw != nullptr ? __ldg(pw + static_cast<size_t>(skb) * p.n_blocks) : 0.f;
+      if (++skb == num_kb) {
+        skb = 0;
+        st += nunits;
+        seek();
+      }
+    };
+    seek();
+    float a0, b0, a1, b1;
+    scales(a0, b0);
+    scales(a1, b1);
 
     bool ok = true;
     for (int t = unit; t < num_tiles; t += nunits) {
@@ -270,37 +295,38 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
-        float a2, b2;
-        scales(t, kb + 2, a2, b2);
         const float f = __fmul_rn(a0, b0);
         const uint64_t f2 = f2_pack(f, f);
         a0 = a1;
         b0 = b1;
-        a1 = a2;
-        b1 = b2;
-        if (!mbar_wait(&tfull[buf], buf_phase, w)) {
+        scales(a1, b1);
+        if (!mbar_wait_inline(&tfull[buf], buf_phase, w)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // sixteen columns are multiplied while the next sixteen are read
+        uint32_t v[2][16];
+        tmem_ld16_issue(tmem_mine + buf * C::BN, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tmem_mine + buf * C::BN + c * 32, v);
-          if (c == 3) {
+        for (int c = 0; c < 8; ++c) {
+          tmem_wait16(v[c & 1]);
+          if (c < 7) {
+            tmem_ld16_issue(tmem_mine + buf * C::BN + (c + 1) * 16, v[(c + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               if constexpr (CG == 1)
                 mbar_arrive(&tempty[buf]);
               else
-                mbar_arrive_cluster(tempty0 + buf * 8u);
+                mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[c * 16 + i] = f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2,
-                                     acc[c * 16 + i]);
+          for (int i = 0; i < 8; ++i)
+            acc[c * 8 + i] = f2_fma(
+                f2_pack(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), f2, acc[c * 8 + i]);
         }
         if (++buf == C::NBUF) {
           buf = 0;
