@@ -25,8 +25,8 @@ namespace fp8mlp {
 
 struct alignas(64) BlockGemmParams {
   CUtensorMap tmA, tmB;
-  CUtensorMap tmOut;   // bf16 output, 32 x 32 tiles
-  CUtensorMap tmOut2;  // relu^2: e4m3 copy, 32 x 32 tiles
+  CUtensorMap tmOut;   // bf16 output, 32 rows x 64 columns
+  CUtensorMap tmOut2;  // relu^2: e4m3 copy, 32 rows x WC columns
   int M, N, K;
   int tiles_m, tiles_n;
   int n_blocks;          // ceil(N / 128): row length of ws
@@ -38,38 +38,45 @@ struct alignas(64) BlockGemmParams {
   int debug_flags;
 };
 
-template <int CG_, int BN_, int STAGES_, bool RELU2_, int NSLOT_>
+// CG CTAs per tile, BN tile columns, WC columns per epilogue warp, NOUT output
+// slots of 64 columns per warp
+template <int CG_, int BN_, int WC_, int STAGES_, bool RELU2_, int NOUT_>
 struct BlockCfg {
   static constexpr int CG = CG_;
   static constexpr int BM = 128;
   static constexpr int TILE_M = BM * CG;
   static constexpr int BN = BN_;
-  static constexpr int B_ROWS = BN / CG;
+  static constexpr int WC = WC_;
+  static constexpr int B_ROWS = BN / CG;           // rows of B per CTA
   static constexpr int STAGES = STAGES_;
   static constexpr bool RELU2 = RELU2_;
-  static constexpr int NSLOT = NSLOT_;
   static constexpr int BK = 128;
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
-  static constexpr int STAGE_TX = CG * (A_BYTES + B_BYTES);
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGE_TX = CG * STAGE_BYTES;
   static constexpr uint32_t IDESC = dev::instr_desc(dev::FMT_E4M3, dev::FMT_E4M3, false, false, TILE_M, BN);
-  static constexpr int NBUF = 512 / BN;  // TMEM accumulators
-  static constexpr int NEPI = 4 * BN / 128;
-  // With eight epilogue warps a thread needs more than 65536 / 384 registers:
-  // the first warpgroup (producer, issuer, two idle warps) hands some over.
-  static constexpr bool SPLIT_REGS = NEPI == 8;
+  static constexpr int NBUF = 512 / BN;            // TMEM accumulators
+  static constexpr int NEPI = 4 * BN / WC;
+  // From eight epilogue warps on a thread needs more than its even share of
+  // the registers: the first warpgroup (producer, issuer, two idle warps)
+  // hands some over.
+  static constexpr bool SPLIT_REGS = NEPI >= 8;
   static constexpr int EPI0 = SPLIT_REGS ? 4 : 2;  // first epilogue warp
   static constexpr int THREADS = 32 * (EPI0 + NEPI);
-  static constexpr int REGS_CONTROL = 56, REGS_EPI = 224;
-  static constexpr int REGS_SUM = 128 * REGS_CONTROL + 256 * REGS_EPI;  // of the launch, at least
-  static constexpr int OUT_BUF = 32 * 32 * 2;
-  static constexpr int SLOT = OUT_BUF + (RELU2 ? 32 * 32 : 0);
+  static constexpr int REGS_CONTROL = NEPI == 16 ? 40 : 56, REGS_EPI = NEPI == 16 ? 104 : 224;
+  static constexpr int REGS_SUM = 128 * REGS_CONTROL + 32 * NEPI * REGS_EPI;  // of the launch, at least
+  // output slots of a warp: 64 columns of bf16 each, and the e4m3 copy
+  static constexpr int OUT_BUF = 32 * 128;
+  static constexpr int NOUT = NOUT_;
+  static constexpr int SLOT = NOUT * OUT_BUF + (RELU2 ? 32 * WC : 0);
+  static constexpr int XCHG_BYTES = RELU2 && WC == 64 ? NEPI * 32 * 4 : 0;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
-  static constexpr int SMEM_BYTES =
-      1024 + STAGES * (A_BYTES + B_BYTES) + NSLOT * NEPI * SLOT + NUM_BARS * 8 + 16;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NEPI * SLOT + XCHG_BYTES + NUM_BARS * 8 + 16;
   static_assert(CG == 1 || CG == 2, "CTA group");
-  static_assert(BN == 128 || BN == 256, "whole weight blocks per epilogue warp");
-  static_assert(B_ROWS % 8 == 0 && SMEM_BYTES <= 232448, "shared memory");
+  static_assert(BN == 128 || BN == 256, "accumulators");
+  static_assert(WC == 128 || WC == 64, "columns per epilogue warp");
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
 namespace dev {
@@ -81,6 +88,22 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A load that stays where it is written: the compiler would sink a plain one
+// to its use, two k-blocks later, and put its latency back into the loop.
+__device__ __forceinline__ float ld_scale(const float* p, bool valid) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
+      "@q ld.global.nc.f32 %0, [%1];\n\t}"
+      : "=f"(v)
+      : "l"(p), "r"(static_cast<int>(valid)));
+  return v;
 }
 
 // max that keeps NaN
@@ -113,10 +136,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   constexpr int CG = C::CG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sA = smem;
-  uint8_t* sB = sA + C::STAGES * C::A_BYTES;
-  uint8_t* sEpi = sB + C::STAGES * C::B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::NSLOT * C::NEPI * C::SLOT);
+  uint8_t* sStage = smem;
+  uint8_t* sEpi = sStage + C::STAGES * C::STAGE_BYTES;
+  float* sXchg = reinterpret_cast<float*>(sEpi + C::NEPI * C::SLOT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::NEPI * C::SLOT + C::XCHG_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + C::NBUF;
@@ -160,104 +183,106 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   const int num_kb = (p.K + C::BK - 1) / C::BK;
 
   if (warp < C::EPI0) {
-  if constexpr (C::SPLIT_REGS) reg_dec<C::REGS_CONTROL>();
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0 && !(p.debug_flags & FP8MLP_DEBUG_STALL_PRODUCER)) {
-      tma_prefetch_desc(&p.tmA);
-      tma_prefetch_desc(&p.tmB);
-      uint32_t stage = 0, phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int t = unit; t < num_tiles && ok; t += nunits) {
-        const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
-        const int m0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM;
-        const int n0 = nb * C::BN + static_cast<int>(rank) * C::B_ROWS;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
-            ok = false;
-            break;
+    if constexpr (C::SPLIT_REGS) reg_dec<C::REGS_CONTROL>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0 && !(p.debug_flags & FP8MLP_DEBUG_STALL_PRODUCER)) {
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+        uint32_t stage = 0, phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = unit; t < num_tiles && ok; t += nunits) {
+          const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+          const int m0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM;
+          const int n0 = nb * C::BN + static_cast<int>(rank) * C::B_ROWS;
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
+              ok = false;
+              break;
+            }
+            uint8_t* a = sStage + stage * C::STAGE_BYTES;
+            uint8_t* b = a + C::A_BYTES;
+            if constexpr (CG == 1) {
+              mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+              tma_load_2d(a, &p.tmA, &full[stage], kb * C::BK, m0);
+              tma_load_2d(b, &p.tmB, &full[stage], kb * C::BK, n0);
+            } else {
+              if (leader) mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
+              const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+              tma_load_2d_cg2(a, &p.tmA, fb, kb * C::BK, m0);
+              tma_load_2d_cg2(b, &p.tmB, fb, kb * C::BK, n0);
+            }
+            ++issued;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          uint8_t* a = sA + stage * C::A_BYTES;
-          uint8_t* b = sB + stage * C::B_BYTES;
-          if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
-            tma_load_2d(a, &p.tmA, &full[stage], kb * C::BK, m0);
-            tma_load_2d(b, &p.tmB, &full[stage], kb * C::BK, n0);
-          } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], C::STAGE_TX);
-            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-            tma_load_2d_cg2(a, &p.tmA, fb, kb * C::BK, m0);
-            tma_load_2d_cg2(b, &p.tmB, fb, kb * C::BK, n0);
-          }
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        }
+        // the last copy into each stage must have landed before exit
+        if (leader) {
+          const long long n_drain = issued < C::STAGES ? issued : C::STAGES;
+          for (long long i = 0; i < n_drain; ++i) {
+            const long long n = issued - 1 - i;
+            mbar_wait_drain(&full[n % C::STAGES], static_cast<uint32_t>((n / C::STAGES) & 1), p.timeout_ns);
           }
         }
       }
-      // the last copy into each stage must have landed before exit
-      if (leader) {
-        const long long n_drain = issued < C::STAGES ? issued : C::STAGES;
-        for (long long i = 0; i < n_drain; ++i) {
-          const long long n = issued - 1 - i;
-          mbar_wait_drain(&full[n % C::STAGES], static_cast<uint32_t>((n / C::STAGES) & 1), p.timeout_ns);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
-      bool ok = true;
-      for (int t = unit; t < num_tiles && ok; t += nunits) {
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait(&tempty[buf], buf_phase ^ 1u, w) || !mbar_wait(&full[stage], phase, w)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * C::A_BYTES);
-          const uint32_t b0 = smem_u32(sB + stage * C::B_BYTES);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0 && leader) {
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+        bool ok = true;
+        for (int t = unit; t < num_tiles && ok; t += nunits) {
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!mbar_wait(&full[stage], phase, w) || !mbar_wait(&tempty[buf], buf_phase ^ 1u, w)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(sStage + stage * C::STAGE_BYTES);
+            const uint32_t b0 = a0 + C::A_BYTES;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024), smem_desc(b0 + k * 32, 16, 1024),
-                           C::IDESC, k != 0 ? 1u : 0u);
-          if constexpr (CG == 1) {
-            tc_commit(&empty[stage]);
-            tc_commit(&tfull[buf]);
-          } else {
-            tc_commit_cg2_mc(&empty[stage], 0x3);
-            tc_commit_cg2_mc(&tfull[buf], 0x3);
-          }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++buf == C::NBUF) {
-            buf = 0;
-            buf_phase ^= 1u;
+            for (int k = 0; k < 4; ++k)
+              umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024),
+                             smem_desc(b0 + k * 32, 16, 1024), C::IDESC, k != 0 ? 1u : 0u);
+            if constexpr (CG == 1) {
+              tc_commit(&tfull[buf]);
+              tc_commit(&empty[stage]);
+            } else {
+              tc_commit_cg2_mc(&tfull[buf], 0x3);
+              tc_commit_cg2_mc(&empty[stage], 0x3);
+            }
+            if (++buf == C::NBUF) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
+        // every UMMA this thread issued must be complete before TMEM is freed
+        if constexpr (CG == 1)
+          tc_commit(fin);
+        else
+          tc_commit_cg2(fin);
+        mbar_wait_drain(fin, 0, p.timeout_ns);
       }
-      // every UMMA this thread issued must be complete before TMEM is freed
-      if constexpr (CG == 1)
-        tc_commit(fin);
-      else
-        tc_commit_cg2(fin);
-      mbar_wait_drain(fin, 0, p.timeout_ns);
     }
-  }
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (C::SPLIT_REGS) reg_inc<C::REGS_EPI>();
     const int q = warp & 3;  // TMEM lane quarter
     const int e = warp - C::EPI0;
-    const int half = e / 4;  // which 128 columns of the tile
-    const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const int c0 = (e >> 2) * C::WC;  // first column of the tile that is this warp's
+    const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0;
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
-    uint32_t buf = 0, buf_phase = 0, ctr = 0;
+    uint8_t* slot = sEpi + e * C::SLOT;
+    const uint32_t sbase = smem_u32(slot);
+    uint32_t buf = 0, buf_phase = 0;
 
     // This thread's two scales, read two k-blocks ahead and across tiles: the
     // next tile's first ones are under way while the current one is written.
@@ -268,13 +293,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
       if (st >= num_tiles) return;
       const int mb = st / p.tiles_n, nb = st - mb * p.tiles_n;
       const int m = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32 + lane;
-      const int nblk = nb * (C::BN / 128) + half;
+      const int nblk = nb * (C::BN / 128) + (c0 >> 7);
       if (m < p.M) px = p.xs + m;
       if (nblk < p.n_blocks) pw = p.ws + nblk;
     };
     auto scales = [&](float& a, float& b) {
-      a = px != nullptr ? __ldg(px + static_cast<size_t>(skb) * p.M) : 0.f;
-      b = pw != nullptr ? __ldg(pw + static_cast<size_t>(skb) * p.n_blocks) : 0.f;
+      a = ld_scale(px + static_cast<size_t>(skb) * p.M, px != nullptr);
+      b = ld_scale(pw + static_cast<size_t>(skb) * p.n_blocks, pw != nullptr);
       if (++skb == num_kb) {
         skb = 0;
         st += nunits;
@@ -290,10 +315,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     for (int t = unit; t < num_tiles; t += nunits) {
       const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
       const int row0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32;
-      const int n0 = nb * C::BN + half * 128;
-      uint64_t acc[64];  // 128 fp32 sums as pairs
+      const int n0 = nb * C::BN + c0;
+      uint64_t acc[C::WC / 2];  // fp32 sums as pairs
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int i = 0; i < C::WC / 2; ++i) acc[i] = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
         const float f = __fmul_rn(a0, b0);
         const uint64_t f2 = f2_pack(f, f);
@@ -307,12 +332,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         tc_fence_after();
         // sixteen columns are multiplied while the next sixteen are read
         uint32_t v[2][16];
-        tmem_ld16_issue(tmem_mine + buf * C::BN, v[0]);
+        const uint32_t src = tmem_mine + buf * C::BN;
+        tmem_ld16_issue(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < C::WC / 16; ++c) {
           tmem_wait16(v[c & 1]);
-          if (c < 7) {
-            tmem_ld16_issue(tmem_mine + buf * C::BN + (c + 1) * 16, v[(c + 1) & 1]);
+          if (c < C::WC / 16 - 1) {
+            tmem_ld16_issue(src + (c + 1) * 16, v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
@@ -341,57 +367,81 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         // rounded once, from the fp32 value.
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < C::WC / 2; ++i) {
           float u, v;
           f2_unpack(acc[i], u, v);
           u = max_nan(u, 0.f);
           v = max_nan(v, 0.f);
-          u = __fmul_rn(u, u);
-          v = __fmul_rn(v, v);
           amax = max_nan(amax, max_nan(u, v));
-          acc[i] = f2_pack(u, v);
+          const uint64_t t = f2_pack(u, v);
+          acc[i] = f2_mul(t, t);
+        }
+        amax = __fmul_rn(amax, amax);  // squaring is monotone, its rounding too
+        if constexpr (C::WC == 64) {
+          // the two warps that share the block exchange their maxima
+          const int pair = ((e >> 3) << 2) + q;
+          sXchg[e * 32 + lane] = amax;
+          named_barrier(1 + pair, 64);
+          amax = max_nan(amax, sXchg[(e ^ 4) * 32 + lane]);
+          named_barrier(1 + pair, 64);
         }
         float inv;
         s = block_scale(amax, &inv);
-        if (row0 + lane < p.M && n0 < p.N) p.post_s[static_cast<size_t>(n0 >> 7) * p.M + row0 + lane] = inv;
+        if ((c0 & 127) == 0 && row0 + lane < p.M && n0 < p.N)
+          p.post_s[static_cast<size_t>(n0 >> 7) * p.M + row0 + lane] = inv;
       }
+      if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have left their slots
+      __syncwarp();
+      // 64 columns of bf16 to a slot and out
+      auto put = [&](int c) {
+        const int off = C::NOUT == 2 ? c * C::OUT_BUF : 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint8_t* slot = sEpi + (e * C::NSLOT + (C::NSLOT == 2 ? (ctr & 1u) : 0u)) * C::SLOT;
-        const uint32_t sbase = smem_u32(slot);
-        if (lane == 0) bulk_wait_read<C::NSLOT - 1>();
-        __syncwarp();
-        uint32_t pk[16];
+        for (int j = 0; j < 8; ++j) {
+          uint32_t pk[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float u, v;
-          f2_unpack(acc[c * 16 + i], u, v);
-          pk[i] = pack_bf16x2(u, v);
-        }
-        store_row_bf16<64>(sbase, lane, pk);
-        if constexpr (C::RELU2) {
-          uint32_t qk[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float u0, u1, u2, u3;
-            f2_unpack(acc[c * 16 + 2 * i], u0, u1);
-            f2_unpack(acc[c * 16 + 2 * i + 1], u2, u3);
-            qk[i] = pack_e4m3x2(__fmul_rn(u0, s), __fmul_rn(u1, s)) |
-                    (pack_e4m3x2(__fmul_rn(u2, s), __fmul_rn(u3, s)) << 16);
+          for (int i = 0; i < 4; ++i) {
+            float u, v;
+            f2_unpack(acc[c * 32 + j * 4 + i], u, v);
+            pk[i] = pack_bf16x2(u, v);
           }
-          const uint32_t qb = sbase + C::OUT_BUF;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            st_shared_v4(qb + swz<1>(lane * 32 + j * 16), qk[4 * j], qk[4 * j + 1], qk[4 * j + 2], qk[4 * j + 3]);
+          st_shared_v4(sbase + off + swz<7>(lane * 128 + j * 16), pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&p.tmOut, slot, n0 + c * 32, row0);
-          if constexpr (C::RELU2) tma_store_2d(&p.tmOut2, slot + C::OUT_BUF, n0 + c * 32, row0);
+          tma_store_2d(&p.tmOut, slot + off, n0 + c * 64, row0);
           bulk_commit();
         }
-        ++ctr;
+      };
+      put(0);
+      if constexpr (C::RELU2) {
+        const uint32_t qb = sbase + C::NOUT * C::OUT_BUF;
+        const uint64_t s2 = f2_pack(s, s);
+#pragma unroll
+        for (int j = 0; j < C::WC / 16; ++j) {
+          uint32_t qk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float u0, u1, u2, u3;
+            f2_unpack(f2_mul(acc[j * 8 + 2 * i], s2), u0, u1);
+            f2_unpack(f2_mul(acc[j * 8 + 2 * i + 1], s2), u2, u3);
+            qk[i] = pack_e4m3x2(u0, u1) | (pack_e4m3x2(u2, u3) << 16);
+          }
+          st_shared_v4(qb + swz<C::WC / 16 - 1>(lane * C::WC + j * 16), qk[0], qk[1], qk[2], qk[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&p.tmOut2, slot + C::NOUT * C::OUT_BUF, n0, row0);
+          bulk_commit();
+        }
+      }
+      if constexpr (C::WC == 128) {
+        if constexpr (C::NOUT == 1) {
+          if (lane == 0) bulk_wait_read<1>();  // the first half has left the slot, the codes may be under way
+          __syncwarp();
+        }
+        put(1);
       }
     }
     if (lane == 0) bulk_wait<0>();
