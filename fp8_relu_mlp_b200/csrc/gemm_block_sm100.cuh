@@ -64,14 +64,14 @@ struct BlockCfg {
   static constexpr bool SPLIT_REGS = NEPI >= 8;
   static constexpr int EPI0 = SPLIT_REGS ? 4 : 2;  // first epilogue warp
   static constexpr int THREADS = 32 * (EPI0 + NEPI);
-  static constexpr int REGS_CONTROL = NEPI == 16 ? 40 : 56, REGS_EPI = NEPI == 16 ? 104 : 224;
+  static constexpr int REGS_CONTROL = 40, REGS_EPI = 232;
   static constexpr int REGS_SUM = 128 * REGS_CONTROL + 32 * NEPI * REGS_EPI;  // of the launch, at least
   // output slots of a warp: 64 columns of bf16 each, and the e4m3 copy
   static constexpr int OUT_BUF = 32 * 128;
   static constexpr int NOUT = NOUT_;
   static constexpr int SLOT = NOUT * OUT_BUF + (RELU2 ? 32 * WC : 0);
   static constexpr int XCHG_BYTES = RELU2 && WC == 64 ? NEPI * 32 * 4 : 0;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + NBUF + 1;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NEPI * SLOT + XCHG_BYTES + NUM_BARS * 8 + 16;
   static_assert(CG == 1 || CG == 2, "CTA group");
   static_assert(BN == 128 || BN == 256, "accumulators");
@@ -113,6 +113,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Scale of a block of 128 whose largest magnitude is `amax`: s maps amax onto
 // 448 and is at most 2^120, so that 1/s stays a normal number; an all-zero
 // block takes s = 1.  A block that holds an infinity or NaN takes s = 1 and
@@ -140,9 +146,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   uint8_t* sEpi = sStage + C::STAGES * C::STAGE_BYTES;
   float* sXchg = reinterpret_cast<float*>(sEpi + C::NEPI * C::SLOT);
   uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::NEPI * C::SLOT + C::XCHG_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + C::NBUF;
+  uint64_t* done = full + C::STAGES;
+  uint64_t* tempty = done + C::STAGES;
   uint64_t* fin = tempty + C::NBUF;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -157,10 +162,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&done[s], 1);
     }
     for (int a = 0; a < C::NBUF; ++a) {
-      mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], C::NEPI * CG);  // one arrival per epilogue warp of the pair
     }
     mbar_init(fin, 1);
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
           const int m0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM;
           const int n0 = nb * C::BN + static_cast<int>(rank) * C::B_ROWS;
           for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, w)) {
+            if (!mbar_wait(&done[stage], phase ^ 1u, w)) {
               ok = false;
               break;
             }
@@ -247,13 +251,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
             for (int k = 0; k < 4; ++k)
               umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024),
                              smem_desc(b0 + k * 32, 16, 1024), C::IDESC, k != 0 ? 1u : 0u);
-            if constexpr (CG == 1) {
-              tc_commit(&tfull[buf]);
-              tc_commit(&empty[stage]);
-            } else {
-              tc_commit_cg2_mc(&tfull[buf], 0x3);
-              tc_commit_cg2_mc(&empty[stage], 0x3);
-            }
+            if constexpr (CG == 1)
+              tc_commit(&done[stage]);
+            else
+              tc_commit_cg2_mc(&done[stage], 0x3);
             if (++buf == C::NBUF) {
               buf = 0;
               buf_phase ^= 1u;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
     uint8_t* slot = sEpi + e * C::SLOT;
     const uint32_t sbase = smem_u32(slot);
-    uint32_t buf = 0, buf_phase = 0;
+    uint32_t buf = 0, stage = 0, phase = 0;
 
     // This thread's two scales, read two k-blocks ahead and across tiles: the
     // next tile's first ones are under way while the current one is written.
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         a0 = a1;
         b0 = b1;
         scales(a1, b1);
-        if (!mbar_wait_inline(&tfull[buf], buf_phase, w)) {
+        if (!mbar_wait_inline(&done[stage], phase, w)) {
           ok = false;
           break;
         }
@@ -354,9 +355,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
             acc[c * 8 + i] = f2_fma(
                 f2_pack(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), f2, acc[c * 8 + i]);
         }
-        if (++buf == C::NBUF) {
-          buf = 0;
-          buf_phase ^= 1u;
+        if (++buf == C::NBUF) buf = 0;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       if (!ok) break;
@@ -370,9 +372,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         for (int i = 0; i < C::WC / 2; ++i) {
           float u, v;
           f2_unpack(acc[i], u, v);
+          amax = max3_nan(amax, u, v);
           u = max_nan(u, 0.f);
           v = max_nan(v, 0.f);
-          amax = max_nan(amax, max_nan(u, v));
           const uint64_t t = f2_pack(u, v);
           acc[i] = f2_mul(t, t);
         }
