@@ -1165,12 +1165,12 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   const NormGateFwd p{M, d, rows_per_gate, eps, r, y, w_post, gate, w_pre, alpha, r_next, x, rstd_post, rstd_pre, xq, xs};
-  const cudaError_t e = launch_norm_gate_fwd(p, di->num_sms, stream);
+  const cudaError_t e = launch_norm_gate_fwd(p, stream);
   return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "norm_gate_fwd launch");
 }
 
 size_t fp8mlp_norm_gate_bwd_workspace_size(int M, int d, int rows_per_gate) {
-  if (M <= 0 || d <= 0 || rows_per_gate <= 0) return 0;
+  if (M <= 0 || d <= 0 || d > kNormMaxD || rows_per_gate <= 0) return 0;
   return norm_gate_bwd_workspace(M, d, rows_per_gate);
 }
 
@@ -1225,7 +1225,7 @@ int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, con
   TRY(current_device(&di));
   const NormGateBwd p{M,  d,       rows_per_gate, r,  y,  w_post,  gate,  w_pre,  alpha,  rstd_post,
                       rstd_pre, r_next, dx, dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, static_cast<float*>(workspace)};
-  const cudaError_t e = launch_norm_gate_bwd(p, di->num_sms, stream);
+  const cudaError_t e = launch_norm_gate_bwd(p, stream);
   return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "norm_gate_bwd launch");
 }
 

@@ -30,7 +30,7 @@ struct NormGateFwd {
   uint8_t* xq;
   float* xs;
 };
-cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, cudaStream_t s);
 
 struct NormGateBwd {
   int M, d, rows;
@@ -43,7 +43,7 @@ struct NormGateBwd {
   float* workspace;
 };
 size_t norm_gate_bwd_workspace(int M, int d, int rows);
-cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, cudaStream_t s);
 
 // optimizer
 cudaError_t launch_adamw_state_init(fp8mlp_adamw_state* st, float lr, unsigned int seed, int step, cudaStream_t s);

@@ -4,10 +4,17 @@
 //   n  = y * rstd(y)               r' = alpha r + gate (n w_post)
 //   x  = r' * rstd(r') * w_pre     (and the e4m3 copy of x, one scale per 1 x 128)
 //
-// Memory-bound: the row is read once into registers, both norms and the
-// quantiser work on it there, and every output is rounded once from fp32.  A
-// worker owns a row: a warp where a lane can hold its share (d <= 1024), else
-// a CTA.
+// Memory-bound: every row is read once, both norms and the quantiser work on
+// it in registers, and every output is rounded once from fp32.  A worker owns
+// a row: 4, 8 or 16 lanes where they can hold it, a warp up to d = 1024, else
+// a CTA.  Workers are persistent and copy their next rows to shared memory
+// while they compute the current one (cp.async, each thread its own 16-byte
+// vectors, so no barrier is needed): the two dependent reductions of a row
+// would otherwise leave HBM idle.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
 #include "block.h"
 
 namespace fp8mlp {
@@ -16,17 +23,33 @@ namespace {
 
 using namespace dev;
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+constexpr int kSmemCta = 224 * 1024;
+constexpr int kRingGateRows = 16;  // gate rows shorter than this are streamed, longer ones stay in registers or L1
+constexpr int kSms = 148;  // CTAs per residency slot; the workspace's size must not depend on the device
+
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&f)[4]) {
   const unsigned int w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16lo_to_f32(w[j]);
-    f[2 * j + 1] = bf16hi_to_f32(w[j]);
-  }
+  for (int j = 0; j < 4; ++j) f[j] = f2_pack(bf16lo_to_f32(w[j]), bf16hi_to_f32(w[j]));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    f2_unpack(f[j], a, b);
+    w[j] = pack_bf16x2(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void product8(const uint4& a, const uint4& b, uint64_t (&f)[4]) {
+  uint64_t x[4], y[4];
+  unpack8(a, x);
+  unpack8(b, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_mul(x[i], y[i]);
 }
 
 __device__ __forceinline__ uint4 ones8() {
@@ -35,14 +58,62 @@ __device__ __forceinline__ uint4 ones8() {
 
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int c) { return *reinterpret_cast<const uint4*>(p + c); }
 
-// sums of N values over the worker's threads; `red` is two buffers used in
-// turn, so that one barrier per call is enough
-template <bool CTA, int N>
-__device__ __forceinline__ void worker_sum(float (&v)[N], float (*red)[32][N], int& turn) {
+// columns c.. of a vector that may be absent (ones); zero past the row's end
+__device__ __forceinline__ uint4 gain8(const uint16_t* p, int c, int d) {
+  if (c >= d) return make_uint4(0, 0, 0, 0);
+  return p != nullptr ? load8(p, c) : ones8();
+}
+
+// 16 bytes to this thread's slot, zeros where `valid` is false
+__device__ __forceinline__ void copy16(uint32_t slot, const uint16_t* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most depth - 1 copy groups are under way
+__device__ __forceinline__ void copy_wait(int depth) {
+  if (depth == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+__device__ __forceinline__ float hsum(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+
+// m / d for m < 2^31 by a product: with 2^(s-1) < d <= 2^s and
+// k = ceil(2^(31+s) / d), m k 2^-(31+s) exceeds m / d by less than 1 / d
+struct FastDiv {
+  uint32_t mul;
+  int shift;  // -1: d = 1
+  __device__ __forceinline__ int operator()(int m) const {
+    return shift < 0 ? m : static_cast<int>(__umulhi(static_cast<uint32_t>(m), mul) >> shift);
+  }
+};
+
+FastDiv fast_div(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  if (s == 0) return {0, -1};
+  return {static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+
+// The ring: each warp has its own, stage by stage the vectors of its 32 lanes
+// next to each other, so that a copy is 512 contiguous bytes and every offset
+// but the stage's is a constant.
+constexpr int kVec = 512;
+
+// Sums of N values over a worker's threads: LPR lanes, or the CTA's warps
+// through `red`, two buffers used in turn, so that one barrier per call is
+// enough.
+template <int LPR, bool CTA, int N>
+__device__ __forceinline__ void worker_sum(float (&v)[N], float (*red)[11][N], int& turn) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int o = LPR / 2; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if constexpr (CTA) {
     const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) {
@@ -60,98 +131,216 @@ __device__ __forceinline__ void worker_sum(float (&v)[N], float (*red)[32][N], i
   }
 }
 
-// VPT 16-byte vectors per thread; CTA: one row per CTA, else one per warp
-template <int VPT, bool CTA>
-__global__ void __launch_bounds__(256) norm_gate_fwd_kernel(const NormGateFwd p) {
+// How rows are dealt out: VPT 16-byte vectors per thread, LPR lanes per row
+// (CTA: all threads of the CTA), `per_sm` CTAs per SM, a ring of `depth` rows.
+// A row's fixed costs (reductions, divisions, addresses) are paid per warp, so
+// a thread takes three or four vectors where the row has them.
+struct NormShape {
+  int vpt, lpr;
+  bool cta;
+  int threads, per_sm, depth;
+  size_t smem;
+};
+
+constexpr int kSmemSm = 227 * 1024, kSmemStatic = 1024 + 1536;  // per CTA: reserved by the system, and declared below
+
+// threads1..4: of a CTA whose workers are warps or less with 1..4 vectors per
+// lane; warps: resident per SM for rows that take a CTA, 3 and 4 vectors per
+// thread; tensors: in the ring; extra: further 16-byte vectors per thread and
+// vector
+NormShape norm_shape(int d, const int (&threads)[4], const int (&warps)[2], int tensors, int extra) {
+  const int nvec = d / 8;
+  NormShape s = {};
+  s.lpr = nvec <= 4 ? 4 : nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
+  s.cta = nvec > 128;
+  s.per_sm = 1;
+  if (!s.cta) {
+    s.vpt = (nvec + 31) / 32;
+    s.threads = threads[s.vpt - 1];
+  } else {
+    const int t3 = (nvec + 95) / 96 * 32, t4 = (nvec + 127) / 128 * 32;
+    s.vpt = 3 * t3 < 4 * t4 ? 3 : 4;
+    s.threads = s.vpt == 3 ? t3 : t4;
+    s.per_sm = std::max(1, warps[s.vpt - 3] * 32 / s.threads);
+  }
+  const size_t stage = static_cast<size_t>(tensors * s.vpt) * 16 * s.threads;
+  const size_t other = static_cast<size_t>(extra) * s.vpt * s.threads * 16 + kSmemStatic;
+  while (s.per_sm > 1 && s.per_sm * (2 * stage + other) > kSmemSm) --s.per_sm;
+  s.depth = s.per_sm * (3 * stage + other) <= kSmemSm ? 3 : 2;
+  s.smem = s.depth * stage + other - kSmemStatic;
+  return s;
+}
+
+// ---- forward ------------------------------------------------------------------
+// `ring_gate`: several gate rows; a row's own is copied ahead like r and y
+template <int VPT, int LPR, bool CTA>
+__global__ void __launch_bounds__(CTA ? 352 : 512) norm_gate_fwd_kernel(const NormGateFwd p, const FastDiv by_rows,
+                                                                        const int depth, const bool ring_gate) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float red[2][32][1];
+  constexpr int kGroupLanes = LPR < 16 ? LPR : 16;  // that hold one scale block (tpr is a multiple of them)
+  constexpr int R = 0, Y = VPT, G = 2 * VPT;        // first vectors of the tensors in the ring
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float red[2][11][1];
   int turn = 0;
-  const int tpr = CTA ? blockDim.x : 32;
-  const int t = CTA ? threadIdx.x : threadIdx.x & 31;
-  const int workers = CTA ? gridDim.x : gridDim.x * (blockDim.x >> 5);
-  const int first = CTA ? blockIdx.x : blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  constexpr int tpr = LPR;  // vectors between two of a thread's; a CTA's warps own runs of 32 VPT vectors
+  const int t = CTA ? (threadIdx.x >> 5) * (32 * VPT) + (threadIdx.x & 31) : threadIdx.x % LPR;
+  constexpr int kPerCta = CTA ? 1 : 512 / LPR;
+  const int workers = gridDim.x * kPerCta;
+  // few rows spread over the CTAs; many are dealt in runs of neighbours, whose
+  // scales share sectors
+  const int first = CTA ? blockIdx.x
+                        : p.M < workers ? blockIdx.x + gridDim.x * (threadIdx.x / LPR)
+                                        : blockIdx.x * kPerCta + threadIdx.x / LPR;
   const bool post = p.y != nullptr, pre = p.x != nullptr;
   const float alpha = p.alpha != nullptr ? *p.alpha : 1.f;
+  const uint64_t alpha2 = f2_pack(alpha, alpha);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  for (int m = first; m < p.M; m += workers) {
-    const size_t base = static_cast<size_t>(m) * p.d;
-    uint4 vr[VPT], vy[VPT];
+  const uint32_t stage_bytes = (ring_gate ? 3 : 2) * VPT * kVec, ring_end = depth * stage_bytes;
+  const char* mine = ring + (threadIdx.x >> 5) * ring_end + (threadIdx.x & 31) * 16;
+  const uint32_t mine32 = smem_u32(mine);
+  auto vec = [&](uint32_t off, int v) { return *reinterpret_cast<const uint4*>(mine + off + v * kVec); };
+  // columns of vector j: col + j * tpr * 8, in the row for j < nv
+  const int col = t * 8;
+  int nv = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = (t + j * tpr) * 8;
-      vr[j] = vy[j] = make_uint4(0, 0, 0, 0);
-      if (c < p.d) {
-        vr[j] = load8(p.r + base, c);
-        if (post) vy[j] = load8(p.y + base, c);
+  for (int j = 0; j < VPT; ++j) nv += col + j * tpr * 8 < p.d ? 1 : 0;
+  auto fetch = [&](uint32_t off, int m) {
+    if (m < p.M) {
+      const size_t base = static_cast<size_t>(m) * p.d + col;
+      const size_t gbase = ring_gate ? static_cast<size_t>(by_rows(m)) * p.d + col : 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const bool in = j < nv;
+        const int o = in ? j * tpr * 8 : 0;  // a vector past the row's end: zeros, from a valid address
+        const size_t a = (nv > 0 ? base : 0) + o;
+        copy16(mine32 + off + (R + j) * kVec, p.r + a, in);
+        if (post) copy16(mine32 + off + (Y + j) * kVec, p.y + a, in);
+        if (ring_gate) copy16(mine32 + off + (G + j) * kVec, p.gate + (nv > 0 ? gbase : 0) + o, in);
       }
     }
-    float rn[VPT][8];
-    float sum[1];
+    copy_commit();
+  };
+  uint4 wpost[VPT], wpre[VPT], gate[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    wpost[j] = gain8(p.w_post, col + j * tpr * 8, p.d);
+    wpre[j] = gain8(p.w_pre, col + j * tpr * 8, p.d);
+    gate[j] = gain8(p.gate, col + j * tpr * 8, p.d);  // the only row, unless the ring brings others
+  }
+  auto next = [&](int m) { return p.M - m > workers ? m + workers : p.M; };
+  int m = first < p.M ? first : p.M, ahead = m;
+  uint32_t off = 0, foff = (depth - 1) * stage_bytes;
+  for (int s = 0; s < depth - 1; ++s) {
+    fetch(s * stage_bytes, ahead);
+    ahead = next(ahead);
+  }
+  // uniform over the warp (a CTA's threads share m)
+  while (__any_sync(0xffffffffu, m < p.M)) {
+    fetch(foff, ahead);
+    ahead = next(ahead);
+    copy_wait(depth);
+    const bool on = m < p.M;
+    const size_t base = static_cast<size_t>(on ? m : 0) * p.d + col;
+    uint64_t rn[VPT][4];
     if (post) {
-      sum[0] = 0.f;
+      if (ring_gate) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        float y[8];
-        unpack8(vy[j], y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[i], y[i], sum[0]);
+        for (int j = 0; j < VPT; ++j) gate[j] = vec(off, G + j);
       }
-      worker_sum<CTA>(sum, red, turn);
-      const float b = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sum[0], inv_d, p.eps)));
-      if (t == 0) p.rstd_post[m] = b;
-      const uint16_t* gate = p.gate != nullptr ? p.gate + static_cast<size_t>(m / p.rows) * p.d : nullptr;
+      uint64_t yy = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = (t + j * tpr) * 8;
-        float r[8], y[8], g[8], wp[8];
-        unpack8(vr[j], r);
-        unpack8(vy[j], y);
-        unpack8(gate != nullptr && c < p.d ? load8(gate, c) : ones8(), g);
-        unpack8(p.w_post != nullptr && c < p.d ? load8(p.w_post, c) : ones8(), wp);
+        uint64_t y[4];
+        unpack8(vec(off, Y + j), y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rn[j][i] = fmaf(g[i], y[i] * b * wp[i], alpha * r[i]);
-        if (c < p.d) *reinterpret_cast<uint4*>(p.r_next + base + c) = pack8(rn[j]);
+        for (int i = 0; i < 4; ++i) yy = f2_fma(y[i], y[i], yy);
+      }
+      float sum[1] = {hsum(yy)};
+      worker_sum<LPR, CTA>(sum, red, turn);
+      const float b = __frsqrt_rn(fmaf(sum[0], inv_d, p.eps));
+      if (on && t == 0) p.rstd_post[m] = b;
+      const uint64_t b2 = f2_pack(b, b);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        uint64_t r[4], y[4], g[4], w[4];
+        unpack8(vec(off, R + j), r);
+        unpack8(vec(off, Y + j), y);
+        unpack8(gate[j], g);
+        unpack8(wpost[j], w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          rn[j][i] = f2_fma(g[i], f2_mul(f2_mul(y[i], b2), w[i]), f2_mul(alpha2, r[i]));
+        if (on && j < nv) *reinterpret_cast<uint4*>(p.r_next + base + j * tpr * 8) = pack8(rn[j]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) unpack8(vr[j], rn[j]);
+      for (int j = 0; j < VPT; ++j) unpack8(vec(off, R + j), rn[j]);
     }
-    if (!pre) continue;
-    sum[0] = 0.f;
+    if (pre) {
+      uint64_t rr = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
+      for (int j = 0; j < VPT; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] = fmaf(rn[j][i], rn[j][i], sum[0]);
-    worker_sum<CTA>(sum, red, turn);
-    const float a = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sum[0], inv_d, p.eps)));
-    if (t == 0) p.rstd_pre[m] = a;
+        for (int i = 0; i < 4; ++i) rr = f2_fma(rn[j][i], rn[j][i], rr);
+      float sum[1] = {hsum(rr)};
+      worker_sum<LPR, CTA>(sum, red, turn);
+      const float a = __frsqrt_rn(fmaf(sum[0], inv_d, p.eps));
+      if (on && t == 0) p.rstd_pre[m] = a;
+      const uint64_t a2 = f2_pack(a, a);
+      float am[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = (t + j * tpr) * 8;
-      float x[8], wp[8];
-      unpack8(p.w_pre != nullptr && c < p.d ? load8(p.w_pre, c) : ones8(), wp);
+      for (int j = 0; j < VPT; ++j) {
+        uint64_t w[4];
+        unpack8(wpre[j], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = rn[j][i] * a * wp[i];
-      if (c < p.d) *reinterpret_cast<uint4*>(p.x + base + c) = pack8(x);
+        for (int i = 0; i < 4; ++i) rn[j][i] = f2_mul(f2_mul(rn[j][i], a2), w[i]);
+        if (on && j < nv) *reinterpret_cast<uint4*>(p.x + base + j * tpr * 8) = pack8(rn[j]);
+        if (p.xq != nullptr) {
+          // sixteen lanes (or the row's few) hold one group of 128 columns
+          am[j] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float u, v;
+            f2_unpack(rn[j][i], u, v);
+            am[j] = max3_nan(am[j], fabsf(u), fabsf(v));
+          }
+#pragma unroll
+          for (int o = kGroupLanes / 2; o > 0; o >>= 1) am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], o));
+        }
+      }
       if (p.xq != nullptr) {
-        // sixteen lanes hold one group of 128 columns
-        float am = 0.f;
+        // lane j of a group works out the scale of its j-th block: two
+        // divisions per row instead of two per vector
+        const int l = t & (kGroupLanes - 1);
+        float top = am[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(x[i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+        for (int j = 1; j < VPT; ++j) top = l == j ? am[j] : top;
         float inv;
-        const float s = block_scale(am, &inv);
-        if (c < p.d) {
+        const float s = block_scale(top, &inv);
+        if (on && l < VPT) {
+          const int c = (t - l + l * tpr) * 8;
+          if (c < p.d) p.xs[static_cast<size_t>(c >> 7) * p.M + m] = inv;
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          const float sj = __shfl_sync(0xffffffffu, s, j, kGroupLanes);
+          const uint64_t s2 = f2_pack(sj, sj);
           uint32_t q[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = pack_e4m3x2(__fmul_rn(x[2 * i], s), __fmul_rn(x[2 * i + 1], s));
-          *reinterpret_cast<uint2*>(p.xq + base + c) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-          if ((t & 15) == 0) p.xs[static_cast<size_t>(c >> 7) * p.M + m] = inv;
+          for (int i = 0; i < 4; ++i) {
+            float u, v;
+            f2_unpack(f2_mul(rn[j][i], s2), u, v);
+            q[i] = pack_e4m3x2(u, v);
+          }
+          if (on && j < nv)
+            *reinterpret_cast<uint2*>(p.xq + base + j * tpr * 8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
         }
       }
     }
+    m = next(m);
+    off = off + stage_bytes == ring_end ? 0 : off + stage_bytes;
+    foff = foff + stage_bytes == ring_end ? 0 : foff + stage_bytes;
   }
 }
 
@@ -162,225 +351,436 @@ __global__ void __launch_bounds__(256) norm_gate_fwd_kernel(const NormGateFwd p)
 //   dr = alpha D
 //   dy = rstd_post (D gw - n c2),            c2 = mean(D gw n)
 // c2 needs D, but mean(D gw n) = mean(E gw n) - rstd_pre c1 mean(xh gw n), so
-// the three sums are taken in one pass and one reduction.  The sums over the
-// rows (gains, gate, alpha) stay in each worker's registers; a worker walks
-// units, a unit being a run of rows of one gate row, and a second kernel adds
-// the workers' parts in a fixed order.
+// the three sums are taken in one pass and one reduction.
+//
+// Sums over rows: a worker takes `len` consecutive rows and keeps
+// T = sum(D n) of the gate row it is in, in registers.  At the end of a gate
+// row (or of its rows) w_post T goes to dgate, or to the workspace where
+// several workers share the gate row, and gate T is added to its part of
+// dw_post.  With one gate row for all, T itself is the worker's part: dgate =
+// w_post sum(T), dw_post = gate sum(T).  The CTA adds its workers' parts, a
+// second kernel those of the CTAs, all in a fixed order.
 struct NormBwdSplit {
-  int workers;  // each owns one partial row of the gains' gradients
-  int slices;   // units per gate row
-  int len;      // rows per unit
-  int groups;   // gate rows
+  int len;           // rows per worker
+  int workers;       // that have rows
+  int ctas, groups;  // gate rows
+  int rpg;           // rows per gate row, at most M
 };
 
-constexpr int kBwdWarpCtas = 296;  // CTAs in warp mode: two per SM
-constexpr int kBwdWarps = 4;
-constexpr int kBwdCtas = 592;      // CTAs in CTA mode: four per SM
+constexpr int kBwdOneCta = 16;    // up to so many rows one CTA does everything, in one launch
+constexpr int kBwdFewGroups = 64;  // a CTA column sums each gate row; beyond, a warp per shared gate row
+constexpr int kBwdGateJobs = 16;
+constexpr int kBwdThreads[4] = {512, 384, 256, 256};
+constexpr int kBwdCtaWarps[2] = {10, 8};  // what the registers allow
 
-__host__ __device__ inline bool bwd_by_cta(int d) { return d > 768; }
+// the shape, with or without the gate in the ring (an address in the
+// workspace must not depend on which: the split is made without it)
+NormShape norm_bwd_shape(int d, int groups, int tensors) {
+  return norm_shape(d, kBwdThreads, kBwdCtaWarps, tensors, groups > 1 ? 2 : 0);
+}
 
 NormBwdSplit norm_bwd_split(int M, int d, int rows) {
   NormBwdSplit s;
-  const int rpg = rows < M ? rows : M;
-  s.groups = (M + rpg - 1) / rpg;
-  const int most = bwd_by_cta(d) ? kBwdCtas : kBwdWarpCtas * kBwdWarps;
-  int n = (most + s.groups - 1) / s.groups;
-  if (n > rpg) n = rpg;
-  s.len = (rpg + n - 1) / n;
-  s.slices = (rpg + s.len - 1) / s.len;
-  const long long units = static_cast<long long>(s.groups) * s.slices;
-  s.workers = units < most ? static_cast<int>(units) : most;
+  s.rpg = rows < M ? rows : M;
+  s.groups = (M + s.rpg - 1) / s.rpg;
+  const NormShape sh = norm_bwd_shape(d, s.groups, 5);
+  const int per_cta = sh.cta ? 1 : sh.threads / sh.lpr;
+  int most = kSms * sh.per_sm * per_cta;
+  if (!sh.cta && M <= kBwdOneCta) most = per_cta;
+  s.len = (M + most - 1) / most;
+  s.workers = (M + s.len - 1) / s.len;
+  const int ctas = most / per_cta;
+  s.ctas = s.workers < ctas ? s.workers : ctas;
   return s;
 }
 
-template <int VPT, bool CTA>
-__global__ void __launch_bounds__(CTA ? 512 : 32 * kBwdWarps) norm_gate_bwd_kernel(const NormGateBwd p, const NormBwdSplit sp) {
+struct NormBwdWorkspace {
+  double* alpha;  // [ctas]
+  float* gain;    // [2][ctas][d]
+  float* gate;    // [workers][2][d], with several gate rows: parts of the gate rows a worker starts and ends in
+};
+
+__host__ __device__ inline size_t bwd_alpha_floats(int ctas) { return 4 * static_cast<size_t>((ctas + 1) / 2); }
+
+__device__ __forceinline__ NormBwdWorkspace bwd_workspace(float* base, int ctas, int d) {
+  NormBwdWorkspace w;
+  w.alpha = reinterpret_cast<double*>(base);
+  w.gain = base + bwd_alpha_floats(ctas);
+  w.gate = w.gain + 2 * static_cast<size_t>(ctas) * d;
+  return w;
+}
+
+__device__ __forceinline__ float4 f32x4(uint64_t lo, uint64_t hi) {
+  float4 f;
+  f2_unpack(lo, f.x, f.y);
+  f2_unpack(hi, f.z, f.w);
+  return f;
+}
+__device__ __forceinline__ void store_f32x8(float* o, const uint64_t (&v)[4]) {
+  *reinterpret_cast<float4*>(o) = f32x4(v[0], v[1]);
+  *reinterpret_cast<float4*>(o + 4) = f32x4(v[2], v[3]);
+}
+
+// The sum over rows for column c, where it goes: a part (`last` false) or the
+// gradients it stands for.
+__device__ __forceinline__ void gain_out(const NormGateBwd& p, const NormBwdWorkspace& ws, int job, bool one, bool last,
+                                         int ctas, int c, float s) {
+  if (!last) {
+    ws.gain[(static_cast<size_t>(job) * ctas + blockIdx.x) * p.d + c] = s;
+  } else if (job == 0) {
+    p.dw_pre[c] = s;
+  } else if (!one) {
+    p.dw_post[c] = s;
+  } else {
+    if (p.dw_post != nullptr) p.dw_post[c] = p.gate != nullptr ? bf16lo_to_f32(p.gate[c]) * s : s;
+    if (p.dgate != nullptr) p.dgate[c] = p.w_post != nullptr ? bf16lo_to_f32(p.w_post[c]) * s : s;
+  }
+}
+
+template <int VPT, int LPR, bool CTA>
+__global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT - 1])
+    norm_gate_bwd_kernel(const NormGateBwd p, const NormBwdSplit sp, const FastDiv by_rpg, const int depth,
+                         const bool ring_gate, const bool direct) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float red[2][32][3];
+  // first vectors of the tensors in the ring: r', dx, dr_next, y, r, gate
+  constexpr int RN = 0, DX = VPT, DR = 2 * VPT, Y = 3 * VPT, R = 4 * VPT, G = 5 * VPT;
+  extern __shared__ __align__(16) uint4 smem[];
+  __shared__ float red[2][11][3];
+  __shared__ double reda[16];
   int turn = 0;
-  const int tpr = CTA ? blockDim.x : 32;
-  const int t = CTA ? threadIdx.x : threadIdx.x & 31;
-  const int me = CTA ? blockIdx.x : blockIdx.x * kBwdWarps + (threadIdx.x >> 5);
-  if (me >= sp.workers) return;  // whole warps (or CTAs) leave
+  const int tid = threadIdx.x, nthr = CTA ? blockDim.x : kBwdThreads[VPT - 1];
+  constexpr int tpr = LPR;  // vectors between two of a thread's; a CTA's warps own runs of 32 VPT vectors
+  const int t = CTA ? (tid >> 5) * (32 * VPT) + (tid & 31) : tid % LPR;
+  const bool one = sp.groups == 1;
   const bool post = p.y != nullptr, pre = p.dx != nullptr;
+  // CTAs first, so that few rows spread out
+  const int me = blockIdx.x + gridDim.x * (CTA ? 0 : tid / LPR);
   const float alpha = p.alpha != nullptr ? *p.alpha : 1.f;
+  const uint64_t alpha2 = f2_pack(alpha, alpha);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  const int rpg = p.rows < p.M ? p.rows : p.M;
-  float* part_gain = p.workspace;  // [2][workers][d]
-  float* part_gate = part_gain + 2 * static_cast<size_t>(sp.workers) * p.d;  // [units][d] when slices > 1
-  float swpre[VPT][8], swpost[VPT][8];
-  double salpha = 0.0;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) swpre[j][i] = swpost[j][i] = 0.f;
-
-  const long long units = static_cast<long long>(sp.groups) * sp.slices;
-  for (long long u = me; u < units; u += sp.workers) {
-    const int g = static_cast<int>(u / sp.slices);
-    const int sl = static_cast<int>(u - static_cast<long long>(g) * sp.slices);
-    const int g0 = g * rpg;  // < M
-    const int gend = p.M - g0 < rpg ? p.M : g0 + rpg;
-    const int m0 = gend - g0 < sl * sp.len ? gend : g0 + sl * sp.len;
-    const int m1 = gend - m0 < sp.len ? gend : m0 + sp.len;
-    float sgate[VPT][8];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sgate[j][i] = 0.f;
-    const uint16_t* gate = p.gate != nullptr ? p.gate + static_cast<size_t>(g) * p.d : nullptr;
-    for (int m = m0; m < m1; ++m) {
-      const size_t base = static_cast<size_t>(m) * p.d;
-      const float a = pre ? p.rstd_pre[m] : 0.f, b = post ? p.rstd_post[m] : 0.f;
-      uint4 vrn[VPT], vdx[VPT], vdr[VPT], vy[VPT], vr[VPT];
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = (t + j * tpr) * 8;
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        vrn[j] = vdx[j] = vdr[j] = vy[j] = vr[j] = z;
-        if (c < p.d) {
-          if (pre) {
-            vrn[j] = load8(p.r_next + base, c);
-            vdx[j] = load8(p.dx + base, c);
-          }
-          if (p.dr_next != nullptr) vdr[j] = load8(p.dr_next + base, c);
-          if (post) vy[j] = load8(p.y + base, c);
-          if (p.dalpha != nullptr) vr[j] = load8(p.r + base, c);
-        }
-      }
-      float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = (t + j * tpr) * 8;
-        float rn[8], dx[8], dr[8], y[8], wpre[8], wpost[8], gt[8];
-        unpack8(vrn[j], rn);
-        unpack8(vdx[j], dx);
-        unpack8(vdr[j], dr);
-        unpack8(vy[j], y);
-        unpack8(p.w_pre != nullptr && c < p.d ? load8(p.w_pre, c) : ones8(), wpre);
-        unpack8(p.w_post != nullptr && c < p.d ? load8(p.w_post, c) : ones8(), wpost);
-        unpack8(gate != nullptr && c < p.d ? load8(gate, c) : ones8(), gt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = rn[i] * a, dxw = dx[i] * wpre[i], gn = gt[i] * wpost[i] * (y[i] * b);
-          s[0] = fmaf(dxw, xh, s[0]);
-          s[1] = fmaf(fmaf(a, dxw, dr[i]), gn, s[1]);
-          s[2] = fmaf(xh, gn, s[2]);
-        }
-      }
-      worker_sum<CTA>(s, red, turn);
-      const float ac1 = a * (s[0] * inv_d);
-      const float c2 = (s[1] - ac1 * s[2]) * inv_d;
-      float row_alpha = 0.f;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = (t + j * tpr) * 8;
-        float rn[8], dx[8], dr[8], y[8], r[8], wpre[8], wpost[8], gt[8], odr[8], ody[8];
-        unpack8(vrn[j], rn);
-        unpack8(vdx[j], dx);
-        unpack8(vdr[j], dr);
-        unpack8(vy[j], y);
-        unpack8(vr[j], r);
-        unpack8(p.w_pre != nullptr && c < p.d ? load8(p.w_pre, c) : ones8(), wpre);
-        unpack8(p.w_post != nullptr && c < p.d ? load8(p.w_post, c) : ones8(), wpost);
-        unpack8(gate != nullptr && c < p.d ? load8(gate, c) : ones8(), gt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = rn[i] * a, n = y[i] * b;
-          const float D = fmaf(-xh, ac1, fmaf(a, dx[i] * wpre[i], dr[i]));
-          odr[i] = alpha * D;
-          ody[i] = b * fmaf(-n, c2, D * gt[i] * wpost[i]);
-          swpre[j][i] = fmaf(dx[i], xh, swpre[j][i]);
-          swpost[j][i] = fmaf(D * gt[i], n, swpost[j][i]);
-          sgate[j][i] = fmaf(D * wpost[i], n, sgate[j][i]);
-          row_alpha = fmaf(D, r[i], row_alpha);
-        }
-        if (c < p.d) {
-          *reinterpret_cast<uint4*>(p.dr + base + c) = pack8(odr);
-          if (post) *reinterpret_cast<uint4*>(p.dy + base + c) = pack8(ody);
-        }
-      }
-      salpha += static_cast<double>(row_alpha);
-    }
-    if (p.dgate != nullptr) {
-      float* out = sp.slices > 1 ? part_gate + static_cast<size_t>(u) * p.d : p.dgate + static_cast<size_t>(g) * p.d;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = (t + j * tpr) * 8;
-        if (c < p.d) {
-          *reinterpret_cast<float4*>(out + c) = make_float4(sgate[j][0], sgate[j][1], sgate[j][2], sgate[j][3]);
-          *reinterpret_cast<float4*>(out + c + 4) = make_float4(sgate[j][4], sgate[j][5], sgate[j][6], sgate[j][7]);
-        }
-      }
-    }
+  const NormBwdWorkspace ws = bwd_workspace(p.workspace, gridDim.x, p.d);
+  // shared memory: this thread's part of dw_post (several gate rows), then the ring
+  uint4* spost = smem + tid;
+  char* ring = reinterpret_cast<char*>(smem + (one ? 0 : 2 * VPT * nthr));
+  const uint32_t stage_bytes = (ring_gate ? 6 : 5) * VPT * kVec, ring_end = depth * stage_bytes;
+  char* mine = ring + (tid >> 5) * ring_end + (tid & 31) * 16;
+  const uint32_t mine32 = smem_u32(mine);
+  auto vec = [&](uint32_t off, int v) { return *reinterpret_cast<const uint4*>(mine + off + v * kVec); };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (!pre || !post || p.dr_next == nullptr || p.dalpha == nullptr) {
+    // tensors that are left out read as zero: nothing is copied over this
+    for (uint32_t o = 0; o < ring_end; o += stage_bytes)
+      for (int v = 0; v < 5 * VPT; ++v) *reinterpret_cast<uint4*>(mine + o + v * kVec) = zero;
   }
+  // one gate row: workers deal out the rows in turn, neighbours to neighbours;
+  // several: `len` consecutive rows each
+  const int all = gridDim.x * (CTA ? 1 : nthr / LPR);
+  const int step = one ? all : 1;
+  const int m0 = one ? min(CTA || p.M < all ? me : static_cast<int>(blockIdx.x) * (nthr / LPR) + tid / LPR, p.M)
+                     : static_cast<int>(min(static_cast<long long>(me) * sp.len, static_cast<long long>(p.M)));
+  const int m1 = one || p.M - m0 < sp.len ? p.M : m0 + sp.len;
+  // columns of vector j: col + j * tpr * 8, in the row for j < nv
+  const int col = t * 8;
+  int nv = 0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) nv += col + j * tpr * 8 < p.d ? 1 : 0;
+  // the row's statistics are read with it, up to two rows ahead
+  float qa[2] = {0.f, 0.f}, qb[2] = {0.f, 0.f};
+  auto fetch = [&](uint32_t off, int m, float& a, float& b) {
+    a = b = 0.f;
+    if (m < m1) {
+      const size_t base = nv > 0 ? static_cast<size_t>(m) * p.d + col : 0;
+      const size_t gbase = ring_gate && nv > 0 ? static_cast<size_t>(by_rpg(m)) * p.d + col : 0;
+      if (pre) a = p.rstd_pre[m];
+      if (post) b = p.rstd_post[m];
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const bool in = j < nv;
+        const int o = in ? j * tpr * 8 : 0;  // a vector past the row's end: zeros, from a valid address
+        const uint32_t dst = mine32 + off + j * kVec;
+        if (pre) {
+          copy16(dst + RN * kVec, p.r_next + base + o, in);
+          copy16(dst + DX * kVec, p.dx + base + o, in);
+        }
+        if (p.dr_next != nullptr) copy16(dst + DR * kVec, p.dr_next + base + o, in);
+        if (post) copy16(dst + Y * kVec, p.y + base + o, in);
+        if (p.dalpha != nullptr) copy16(dst + R * kVec, p.r + base + o, in);
+        if (ring_gate) copy16(dst + G * kVec, p.gate + gbase + o, in);
+      }
+    }
+    copy_commit();
+  };
+
+  uint4 wpre[VPT], wpost[VPT], gate[VPT];
+  uint64_t gw[VPT][4], swpre[VPT][4], T[VPT][4];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int c = (t + j * tpr) * 8;
-    if (c < p.d) {
-      float* o = part_gain + static_cast<size_t>(me) * p.d + c;
-      float* o2 = o + static_cast<size_t>(sp.workers) * p.d;
-      if (p.dw_pre != nullptr) {
-        *reinterpret_cast<float4*>(o) = make_float4(swpre[j][0], swpre[j][1], swpre[j][2], swpre[j][3]);
-        *reinterpret_cast<float4*>(o + 4) = make_float4(swpre[j][4], swpre[j][5], swpre[j][6], swpre[j][7]);
+    const int c = col + j * tpr * 8;
+    wpre[j] = gain8(p.w_pre, c, p.d);
+    wpost[j] = gain8(p.w_post, c, p.d);
+    gate[j] = zero;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gw[j][i] = swpre[j][i] = T[j][i] = 0;
+    if (!one) spost[(2 * j) * nthr] = spost[(2 * j + 1) * nthr] = zero;
+  }
+  double salpha = 0.0;
+  const int g_first = by_rpg(m0 < p.M ? m0 : 0);
+  int g = -1;      // gate row of T
+  int g_end = m0;  // where it ends
+  // T of gate row g to its place, and its share of dw_post
+  auto flush = [&]() {
+    const bool whole = g * static_cast<long long>(sp.rpg) >= m0 && g_end <= m1;
+    float* dst = nullptr;
+    if (p.dgate != nullptr)
+      dst = whole ? p.dgate + static_cast<size_t>(g) * p.d
+                  : ws.gate + (2 * static_cast<size_t>(me) + (g == g_first ? 0 : 1)) * p.d;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      uint64_t w[4], o[4], f[4];
+      unpack8(wpost[j], w);
+      unpack8(gate[j], f);
+      const uint4 a = spost[(2 * j) * nthr], b = spost[(2 * j + 1) * nthr];
+      uint64_t s[4] = {f2_pack(__uint_as_float(a.x), __uint_as_float(a.y)), f2_pack(__uint_as_float(a.z), __uint_as_float(a.w)),
+                       f2_pack(__uint_as_float(b.x), __uint_as_float(b.y)), f2_pack(__uint_as_float(b.z), __uint_as_float(b.w))};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] = f2_mul(T[j][i], w[i]);
+        s[i] = f2_fma(T[j][i], f[i], s[i]);
+        T[j][i] = 0;
       }
-      if (p.dw_post != nullptr) {
-        *reinterpret_cast<float4*>(o2) = make_float4(swpost[j][0], swpost[j][1], swpost[j][2], swpost[j][3]);
-        *reinterpret_cast<float4*>(o2 + 4) = make_float4(swpost[j][4], swpost[j][5], swpost[j][6], swpost[j][7]);
+      if (dst != nullptr && j < nv) store_f32x8(dst + col + j * tpr * 8, o);
+      *reinterpret_cast<float4*>(&spost[(2 * j) * nthr]) = f32x4(s[0], s[1]);
+      *reinterpret_cast<float4*>(&spost[(2 * j + 1) * nthr]) = f32x4(s[2], s[3]);
+    }
+  };
+
+  int m = m0, ahead = m0;
+  uint32_t off = 0, foff = (depth - 1) * stage_bytes;
+  auto next = [&](int k) { return m1 - k > step ? k + step : m1; };
+  fetch(0, ahead, qa[0], qb[0]);
+  ahead = next(ahead);
+  if (depth == 3) {
+    fetch(stage_bytes, ahead, qa[1], qb[1]);
+    ahead = next(ahead);
+  }
+  // uniform over the warp (a CTA's threads share m)
+  while (__any_sync(0xffffffffu, m < m1)) {
+    float fa, fb;
+    fetch(foff, ahead, fa, fb);
+    ahead = next(ahead);
+    const bool on = m < m1;
+    if (on && m >= g_end && post) {
+      // the next gate row
+      if (!one && g >= 0) flush();
+      g = by_rpg(m);
+      g_end = p.M - g * sp.rpg < sp.rpg ? p.M : (g + 1) * sp.rpg;
+      if (!ring_gate) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          gate[j] = gain8(p.gate != nullptr ? p.gate + static_cast<size_t>(g) * p.d : nullptr, col + j * tpr * 8, p.d);
+          product8(gate[j], wpost[j], gw[j]);
+        }
+      }
+    }
+    copy_wait(depth);
+    if (ring_gate && on) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        gate[j] = vec(off, G + j);
+        product8(gate[j], wpost[j], gw[j]);
+      }
+    }
+    const size_t base = static_cast<size_t>(on ? m : 0) * p.d + col;
+    const float a = qa[0], b = qb[0];
+    const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
+    uint64_t s0 = 0, s1 = 0, s2 = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      uint64_t rn[4], dx[4], dr[4], y[4], w[4];
+      unpack8(vec(off, RN + j), rn);
+      unpack8(vec(off, DX + j), dx);
+      unpack8(vec(off, DR + j), dr);
+      unpack8(vec(off, Y + j), y);
+      unpack8(wpre[j], w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t xh = f2_mul(rn[i], a2), dxw = f2_mul(dx[i], w[i]), gn = f2_mul(gw[j][i], f2_mul(y[i], b2));
+        s0 = f2_fma(dxw, xh, s0);
+        s1 = f2_fma(f2_fma(a2, dxw, dr[i]), gn, s1);
+        s2 = f2_fma(xh, gn, s2);
+      }
+    }
+    float s[3] = {hsum(s0), hsum(s1), hsum(s2)};
+    worker_sum<LPR, CTA>(s, red, turn);
+    const float ac1 = a * (s[0] * inv_d);
+    const float c2 = (s[1] - ac1 * s[2]) * inv_d;
+    const uint64_t nac1 = f2_pack(-ac1, -ac1), nc2 = f2_pack(-c2, -c2);
+    asm volatile("" ::: "memory");  // the vectors are read again: kept, they would spill
+    uint64_t ra = 0;
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        uint64_t rn[4], dx[4], dr[4], y[4], r[4], w[4], odr[4], ody[4];
+        unpack8(vec(off, RN + j), rn);
+        unpack8(vec(off, DX + j), dx);
+        unpack8(vec(off, DR + j), dr);
+        unpack8(vec(off, Y + j), y);
+        unpack8(vec(off, R + j), r);
+        unpack8(wpre[j], w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t xh = f2_mul(rn[i], a2), n = f2_mul(y[i], b2);
+          const uint64_t D = f2_fma(xh, nac1, f2_fma(a2, f2_mul(dx[i], w[i]), dr[i]));
+          odr[i] = f2_mul(alpha2, D);
+          ody[i] = f2_mul(b2, f2_fma(n, nc2, f2_mul(D, gw[j][i])));
+          swpre[j][i] = f2_fma(dx[i], xh, swpre[j][i]);
+          T[j][i] = f2_fma(D, n, T[j][i]);
+          ra = f2_fma(D, r[i], ra);
+        }
+        if (j < nv) {
+          *reinterpret_cast<uint4*>(p.dr + base + j * tpr * 8) = pack8(odr);
+          if (post) *reinterpret_cast<uint4*>(p.dy + base + j * tpr * 8) = pack8(ody);
+        }
+      }
+      salpha += static_cast<double>(hsum(ra));
+    }
+    qa[0] = depth == 2 ? fa : qa[1];
+    qb[0] = depth == 2 ? fb : qb[1];
+    qa[1] = fa;
+    qb[1] = fb;
+    m = next(m);
+    off = off + stage_bytes == ring_end ? 0 : off + stage_bytes;
+    foff = foff + stage_bytes == ring_end ? 0 : foff + stage_bytes;
+  }
+  if (!one && g >= 0) flush();
+
+  // ---- the CTA's parts of dw_pre (job 0) and of T or dw_post (job 1)
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+  for (int job = 0; job < 2; ++job) {
+    if (job == 0 ? p.dw_pre == nullptr : (p.dw_post == nullptr && !(one && p.dgate != nullptr))) continue;
+    uint64_t v[VPT][4];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (job == 1 && !one) {
+        const uint4 a = spost[(2 * j) * nthr], b = spost[(2 * j + 1) * nthr];
+        v[j][0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
+        v[j][1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[j][2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));
+        v[j][3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = job == 0 ? swpre[j][i] : T[j][i];
+      }
+    }
+    if constexpr (!CTA) {
+      // over a warp's workers by shuffles, over the warps through the ring
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int o = LPR; o < 32; o <<= 1) v[j][i] = f2_add(v[j][i], __shfl_xor_sync(0xffffffffu, v[j][i], o));
+      const int warp = tid >> 5, nw = nthr >> 5;
+      float* buf = reinterpret_cast<float*>(ring);
+      const int width = LPR * VPT * 8;
+      __syncthreads();  // the ring (and the other job's sums) are done with
+      if ((tid & 31) < LPR) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) store_f32x8(buf + warp * width + (t + j * LPR) * 8, v[j]);
+      }
+      __syncthreads();
+      for (int c = tid; c < p.d; c += nthr) {
+        float s = 0.f;
+        for (int k = 0; k < nw; ++k) s += buf[k * width + c];
+        gain_out(p, ws, job, one, direct, gridDim.x, c, s);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = (t + j * tpr) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x, y;
+          f2_unpack(v[j][i], x, y);
+          if (c < p.d) {
+            gain_out(p, ws, job, one, direct, gridDim.x, c + 2 * i, x);
+            gain_out(p, ws, job, one, direct, gridDim.x, c + 2 * i + 1, y);
+          }
+        }
       }
     }
   }
   if (p.dalpha != nullptr) {
-    double* part_alpha = reinterpret_cast<double*>(part_gate + (sp.slices > 1 ? static_cast<size_t>(units) * p.d : 0));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) salpha += __shfl_xor_sync(0xffffffffu, salpha, o);
-    if constexpr (CTA) {
-      __shared__ double reda[32];
-      if ((threadIdx.x & 31) == 0) reda[threadIdx.x >> 5] = salpha;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        salpha = 0.0;
-        for (int k = 0; k < static_cast<int>(blockDim.x >> 5); ++k) salpha += reda[k];
-      }
+    if ((tid & 31) == 0) reda[tid >> 5] = salpha;
+    __syncthreads();
+    if (tid == 0) {
+      salpha = 0.0;
+      for (int k = 0; k < nthr >> 5; ++k) salpha += reda[k];
+      if (direct)
+        *p.dalpha = static_cast<float>(salpha);
+      else
+        ws.alpha[blockIdx.x] = salpha;
     }
-    if (t == 0) part_alpha[me] = salpha;
   }
 }
 
-// Adds the workers' parts: blockIdx.y = 0, 1 the gains, 2.. the gate rows
-// (when they were split).  32 columns x 32 interleaved partial sums per CTA.
+// Adds the CTAs' parts: blockIdx.y = 0, 1 the gains, 2.. gate rows that several
+// workers share.  32 columns x 32 interleaved partial sums per CTA; beyond
+// kBwdFewGroups gate rows a warp adds one gate row's few parts.
 __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateBwd p, const NormBwdSplit sp) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  const float* part_gate = p.workspace + 2 * static_cast<size_t>(sp.workers) * p.d;
+  const NormBwdWorkspace ws = bwd_workspace(p.workspace, sp.ctas, p.d);
   const int job = blockIdx.y;
+  const bool one = sp.groups == 1;
   if (p.dalpha != nullptr && blockIdx.x == 0 && job == 0 && row == 31) {
-    const size_t units = static_cast<size_t>(sp.groups) * sp.slices;
-    const double* pa = reinterpret_cast<const double*>(part_gate + (sp.slices > 1 ? units * p.d : 0));
     double s = 0.0;
-    for (int k = lane; k < sp.workers; k += 32) s += pa[k];
+    for (int k = lane; k < sp.ctas; k += 32) s += ws.alpha[k];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) *p.dalpha = static_cast<float>(s);
   }
-  float* out = job == 0 ? p.dw_pre : job == 1 ? p.dw_post : p.dgate + static_cast<size_t>(job - 2) * p.d;
-  if (out == nullptr) return;
+  if (job >= 2 && sp.groups > kBwdFewGroups) {
+    for (int w = 1 + (job - 2) * 32 + row; w < sp.workers; w += kBwdGateJobs * 32) {
+      const int b = w * sp.len, g = b / sp.rpg;
+      const long long r0 = static_cast<long long>(g) * sp.rpg;
+      if (r0 == b || r0 / sp.len != w - 1) continue;  // not shared, or not the first worker after its owner
+      const long long r1 = min(r0 + sp.rpg, static_cast<long long>(p.M));
+      const int last = static_cast<int>((r1 - 1) / sp.len);
+      if (c >= p.d) continue;
+      float s = ws.gate[(2 * static_cast<size_t>(w - 1) + (static_cast<long long>(w - 1) * sp.len / sp.rpg == g ? 0 : 1)) * p.d + c];
+      for (int k = w; k <= last; ++k) s += ws.gate[2 * static_cast<size_t>(k) * p.d + c];
+      p.dgate[static_cast<size_t>(g) * p.d + c] = s;
+    }
+    return;
+  }
   const float* src;
-  int n;
+  size_t stride = p.d;
+  int n, first = 0;  // parts, and which of the first worker's two is meant
   if (job < 2) {
-    src = p.workspace + static_cast<size_t>(job) * sp.workers * p.d;
-    n = sp.workers;
+    if (job == 0 ? p.dw_pre == nullptr : (p.dw_post == nullptr && !(one && p.dgate != nullptr))) return;
+    src = ws.gain + static_cast<size_t>(job) * sp.ctas * p.d;
+    n = sp.ctas;
   } else {
-    src = part_gate + static_cast<size_t>(job - 2) * sp.slices * p.d;
-    n = sp.slices;
+    const int g = job - 2;
+    const long long r0 = static_cast<long long>(g) * sp.rpg, r1 = min(r0 + sp.rpg, static_cast<long long>(p.M));
+    const int w0 = static_cast<int>(r0 / sp.len), w1 = static_cast<int>((r1 - 1) / sp.len);
+    if (w0 == w1) return;  // written by its only worker
+    src = ws.gate + 2 * static_cast<size_t>(w0) * p.d;
+    stride = 2 * static_cast<size_t>(p.d);
+    n = w1 - w0 + 1;
+    first = static_cast<long long>(w0) * sp.len / sp.rpg == g ? 0 : 1;
   }
   float s = 0.f;
   if (c < p.d)
-    for (int k = row; k < n; k += 32) s += src[static_cast<size_t>(k) * p.d + c];
+    for (int k = row; k < n; k += 32) s += src[k * stride + (k == 0 ? first * static_cast<size_t>(p.d) : 0) + c];
   sh[row][lane] = s;
   __syncthreads();
   // transposed: warp `row` adds column `row`
@@ -388,76 +788,105 @@ __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateB
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const int col = blockIdx.x * 32 + row;
-  if (lane == 0 && col < p.d) out[col] = s;
+  if (lane == 0 && col < p.d) {
+    if (job < 2)
+      gain_out(p, ws, job, one, true, sp.ctas, col, s);
+    else
+      p.dgate[static_cast<size_t>(job - 2) * p.d + col] = s;
+  }
 }
 
-template <int VPT, bool CTA>
-cudaError_t fwd_one(const NormGateFwd& p, int grid, int threads, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(norm_gate_fwd_kernel<VPT, CTA>, dim3(grid), dim3(threads), 0, s, p);
+// sets a kernel's shared memory limit once per device; two threads racing here
+// set the same value
+template <class F>
+cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCta);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <int VPT, int LPR, bool CTA>
+cudaError_t fwd_one(const NormGateFwd& p, const NormShape& sh, bool ring_gate, cudaStream_t s) {
+  static std::atomic<bool> done[64] = {};
+  cudaError_t e = allow_smem(norm_gate_fwd_kernel<VPT, LPR, CTA>, done);
+  if (e != cudaSuccess) return e;
+  const int most = kSms * sh.per_sm;
+  e = launch_pdl(norm_gate_fwd_kernel<VPT, LPR, CTA>, dim3(p.M < most ? p.M : most), dim3(sh.threads), sh.smem, s, p,
+                 fast_div(p.rows), sh.depth, ring_gate);
   count_launches(1);
   return e;
 }
 
-template <int VPT, bool CTA>
-cudaError_t bwd_one(const NormGateBwd& p, const NormBwdSplit& sp, int threads, cudaStream_t s) {
-  const int grid = CTA ? sp.workers : (sp.workers + kBwdWarps - 1) / kBwdWarps;
-  const cudaError_t e = launch_pdl(norm_gate_bwd_kernel<VPT, CTA>, dim3(grid), dim3(threads), 0, s, p, sp);
+template <int VPT, int LPR, bool CTA>
+cudaError_t bwd_one(const NormGateBwd& p, const NormBwdSplit& sp, const NormShape& sh, bool ring_gate, bool direct,
+                    cudaStream_t s) {
+  static std::atomic<bool> done[64] = {};
+  cudaError_t e = allow_smem(norm_gate_bwd_kernel<VPT, LPR, CTA>, done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(norm_gate_bwd_kernel<VPT, LPR, CTA>, dim3(sp.ctas), dim3(sh.threads), sh.smem, s, p, sp,
+                 fast_div(sp.rpg), sh.depth, ring_gate, direct);
   count_launches(1);
   return e;
 }
 
-int threads_for(int nvec, int vpt) { return (nvec + 32 * vpt - 1) / (32 * vpt) * 32; }
+template <class F>
+cudaError_t by_shape(const NormShape& s, F&& f) {
+  using std::integral_constant;
+  if (s.cta) {
+    if (s.vpt == 3) return f(integral_constant<int, 3>(), integral_constant<int, 32>(), std::true_type());
+    return f(integral_constant<int, 4>(), integral_constant<int, 32>(), std::true_type());
+  }
+  if (s.lpr == 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>(), std::false_type());
+  if (s.lpr == 8) return f(integral_constant<int, 1>(), integral_constant<int, 8>(), std::false_type());
+  if (s.lpr == 16) return f(integral_constant<int, 1>(), integral_constant<int, 16>(), std::false_type());
+  if (s.vpt == 1) return f(integral_constant<int, 1>(), integral_constant<int, 32>(), std::false_type());
+  if (s.vpt == 2) return f(integral_constant<int, 2>(), integral_constant<int, 32>(), std::false_type());
+  if (s.vpt == 3) return f(integral_constant<int, 3>(), integral_constant<int, 32>(), std::false_type());
+  return f(integral_constant<int, 4>(), integral_constant<int, 32>(), std::false_type());
+}
 
 }  // namespace
 
-cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, int num_sms, cudaStream_t s) {
-  const int nvec = p.d / 8;
-  if (nvec <= 128) {
-    // a warp per row, eight rows per CTA
-    const int need = (p.M + 7) / 8, most = num_sms * 8;
-    const int grid = need < most ? need : most;
-    if (nvec <= 32) return fwd_one<1, false>(p, grid, 256, s);
-    if (nvec <= 64) return fwd_one<2, false>(p, grid, 256, s);
-    if (nvec <= 96) return fwd_one<3, false>(p, grid, 256, s);
-    return fwd_one<4, false>(p, grid, 256, s);
-  }
-  const int most = num_sms * 16;
-  const int grid = p.M < most ? p.M : most;
-  if (nvec <= 256) return fwd_one<1, true>(p, grid, threads_for(nvec, 1), s);
-  if (nvec <= 512) return fwd_one<2, true>(p, grid, threads_for(nvec, 2), s);
-  return fwd_one<4, true>(p, grid, threads_for(nvec, 4), s);
+cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, cudaStream_t s) {
+  const bool ring_gate = p.gate != nullptr && p.rows < p.M;
+  const int threads[4] = {512, 512, 512, 512}, cta_warps[2] = {12, 12};
+  const NormShape sh = norm_shape(p.d, threads, cta_warps, ring_gate ? 3 : 2, 0);
+  return by_shape(sh, [&](auto vpt, auto lpr, auto cta) {
+    return fwd_one<decltype(vpt)::value, decltype(lpr)::value, decltype(cta)::value>(p, sh, ring_gate, s);
+  });
 }
 
 size_t norm_gate_bwd_workspace(int M, int d, int rows) {
   const NormBwdSplit sp = norm_bwd_split(M, d, rows);
-  const size_t units = static_cast<size_t>(sp.groups) * sp.slices;
-  const size_t floats = (2 * static_cast<size_t>(sp.workers) + (sp.slices > 1 ? units : 0)) * d;
-  return floats * 4 + static_cast<size_t>(sp.workers) * 8;
+  const size_t rows_of_parts = 2 * static_cast<size_t>(sp.ctas) + (sp.groups > 1 ? 2 * static_cast<size_t>(sp.workers) : 0);
+  return (bwd_alpha_floats(sp.ctas) + rows_of_parts * d) * sizeof(float);
 }
 
-cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, int num_sms, cudaStream_t s) {
-  (void)num_sms;
+cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, cudaStream_t s) {
   const NormBwdSplit sp = norm_bwd_split(p.M, p.d, p.rows);
-  const int nvec = p.d / 8;
-  cudaError_t e;
-  if (!bwd_by_cta(p.d)) {
-    const int threads = 32 * kBwdWarps;
-    if (nvec <= 32)
-      e = bwd_one<1, false>(p, sp, threads, s);
-    else if (nvec <= 64)
-      e = bwd_one<2, false>(p, sp, threads, s);
-    else
-      e = bwd_one<3, false>(p, sp, threads, s);
-  } else if (nvec <= 256) {
-    e = bwd_one<1, true>(p, sp, threads_for(nvec, 1), s);
-  } else {
-    e = bwd_one<2, true>(p, sp, threads_for(nvec, 2), s);
-  }
-  if (e != cudaSuccess) return e;
-  const bool gate_parts = p.dgate != nullptr && sp.slices > 1;
-  if (p.dw_pre == nullptr && p.dw_post == nullptr && !gate_parts && p.dalpha == nullptr) return cudaSuccess;
-  const dim3 grid((p.d + 31) / 32, 2 + (gate_parts ? sp.groups : 0));
-  e = launch_pdl(norm_gate_bwd_sum_kernel, grid, dim3(1024), 0, s, p, sp);
+  // gate rows that several workers share
+  const bool gate_parts = p.dgate != nullptr && sp.groups > 1 && sp.len % sp.rpg != 0;
+  const bool direct = sp.ctas == 1 && !gate_parts;
+  // the gate in the ring too, where its rows are short and the ring still holds two rows of everything
+  NormShape sh = norm_bwd_shape(p.d, sp.groups, 6);
+  const bool ring_gate =
+      p.gate != nullptr && sp.rpg < kRingGateRows && sp.groups > 1 && sh.smem <= static_cast<size_t>(kSmemCta);
+  if (!ring_gate) sh = norm_bwd_shape(p.d, sp.groups, 5);
+  cudaError_t e = by_shape(sh, [&](auto vpt, auto lpr, auto cta) {
+    return bwd_one<decltype(vpt)::value, decltype(lpr)::value, decltype(cta)::value>(p, sp, sh, ring_gate, direct, s);
+  });
+  if (e != cudaSuccess || direct) return e;
+  const bool one_gate = p.dgate != nullptr && sp.groups == 1;
+  if (p.dw_pre == nullptr && p.dw_post == nullptr && !one_gate && !gate_parts && p.dalpha == nullptr) return e;
+  const int jobs = 2 + (!gate_parts ? 0 : sp.groups > kBwdFewGroups ? kBwdGateJobs : sp.groups);
+  e = launch_pdl(norm_gate_bwd_sum_kernel, dim3((p.d + 31) / 32, jobs), dim3(1024), 0, s, p, sp);
   count_launches(1);
   return e;
 }
