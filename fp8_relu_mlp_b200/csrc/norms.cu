@@ -148,7 +148,7 @@ constexpr int kSmemSm = 227 * 1024, kSmemStatic = 1024 + 1536;  // per CTA: rese
 // lane; warps: resident per SM for rows that take a CTA, 3 and 4 vectors per
 // thread; tensors: in the ring; extra: further 16-byte vectors per thread and
 // vector
-NormShape norm_shape(int d, const int (&threads)[4], const int (&warps)[2], int tensors, int extra) {
+NormShape norm_shape(int d, const int (&threads)[4], const int (&vpts)[2], const int (&warps)[2], int largest, int tensors, int extra) {
   const int nvec = d / 8;
   NormShape s = {};
   s.lpr = nvec <= 4 ? 4 : nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
@@ -158,10 +158,12 @@ NormShape norm_shape(int d, const int (&threads)[4], const int (&warps)[2], int 
     s.vpt = (nvec + 31) / 32;
     s.threads = threads[s.vpt - 1];
   } else {
-    const int t3 = (nvec + 95) / 96 * 32, t4 = (nvec + 127) / 128 * 32;
-    s.vpt = 3 * t3 < 4 * t4 ? 3 : 4;
-    s.threads = s.vpt == 3 ? t3 : t4;
-    s.per_sm = std::max(1, warps[s.vpt - 3] * 32 / s.threads);
+    // the smaller VPT unless it takes a larger CTA than there is, or wastes more lanes
+    const int ta = (nvec + 32 * vpts[0] - 1) / (32 * vpts[0]) * 32, tb = (nvec + 32 * vpts[1] - 1) / (32 * vpts[1]) * 32;
+    const int k = ta > largest || vpts[0] * ta > vpts[1] * tb ? 1 : 0;
+    s.vpt = vpts[k];
+    s.threads = k == 0 ? ta : tb;
+    s.per_sm = std::max(1, warps[k] * 32 / s.threads);
   }
   const size_t stage = static_cast<size_t>(tensors * s.vpt) * 16 * s.threads;
   const size_t other = static_cast<size_t>(extra) * s.vpt * s.threads * 16 + kSmemStatic;
@@ -174,7 +176,7 @@ NormShape norm_shape(int d, const int (&threads)[4], const int (&warps)[2], int 
 // ---- forward ------------------------------------------------------------------
 // `ring_gate`: several gate rows; a row's own is copied ahead like r and y
 template <int VPT, int LPR, bool CTA>
-__global__ void __launch_bounds__(CTA ? 352 : 512) norm_gate_fwd_kernel(const NormGateFwd p, const FastDiv by_rows,
+__global__ void __launch_bounds__(CTA ? 384 : 512) norm_gate_fwd_kernel(const NormGateFwd p, const FastDiv by_rows,
                                                                         const int depth, const bool ring_gate) {
   pdl_wait();
   pdl_launch_dependents();
@@ -353,51 +355,80 @@ __global__ void __launch_bounds__(CTA ? 352 : 512) norm_gate_fwd_kernel(const No
 // c2 needs D, but mean(D gw n) = mean(E gw n) - rstd_pre c1 mean(xh gw n), so
 // the three sums are taken in one pass and one reduction.
 //
-// Sums over rows: a worker takes `len` consecutive rows and keeps
-// T = sum(D n) of the gate row it is in, in registers.  At the end of a gate
-// row (or of its rows) w_post T goes to dgate, or to the workspace where
-// several workers share the gate row, and gate T is added to its part of
-// dw_post.  With one gate row for all, T itself is the worker's part: dgate =
-// w_post sum(T), dw_post = gate sum(T).  The CTA adds its workers' parts, a
-// second kernel those of the CTAs, all in a fixed order.
+// Sums over rows: a worker keeps T = sum(D n) of the gate row it is in, in
+// registers.  At the gate row's end w_post T goes to dgate, or to the
+// workspace where several workers share the gate row, and gate T is added to
+// its part of dw_post.  With one gate row for all, T itself is the worker's
+// part: dgate = w_post sum(T), dw_post = gate sum(T).  The CTA adds its
+// workers' parts, a second kernel those of the CTAs, all in a fixed order.
+//
+// The rows are cut into one run per team of workers, and a team deals out its
+// run's rows in turn, so that what is in flight lies close together: a run
+// per worker instead, 14 rows of 768, took 51 us where this takes 37
+// (16384 x 768), as HBM then opens a page for each worker.  Larger teams share
+// more gate rows: a worker leaves one part per gate row of its team's run.
 struct NormBwdSplit {
-  int len;           // rows per worker
-  int workers;       // that have rows
   int ctas, groups;  // gate rows
   int rpg;           // rows per gate row, at most M
+  int team, run;     // workers per team, rows per team
+  int unit;          // neighbouring rows dealt at once: 1, or a whole gate row
+  int slots;         // parts of gate rows per worker: of the most that a run touches
+  int spread;        // 1: fewer rows than workers, workers counted across the CTAs
 };
 
 constexpr int kBwdOneCta = 16;    // up to so many rows one CTA does everything, in one launch
-constexpr int kBwdFewGroups = 64;  // a CTA column sums each gate row; beyond, a warp per shared gate row
-constexpr int kBwdGateJobs = 16;
+constexpr int kBwdFewGroups = 64;  // a CTA column sums each gate row; beyond, a warp
+constexpr int kBwdUnit = 32;       // gate rows up to this length may be dealt whole
 constexpr int kBwdThreads[4] = {512, 384, 256, 256};
-constexpr int kBwdCtaWarps[2] = {10, 8};  // what the registers allow
+constexpr int kBwdCtaVpt[2] = {2, 4}, kBwdCtaWarps[2] = {16, 8};  // what the registers allow
 
-// the shape, with or without the gate in the ring (an address in the
-// workspace must not depend on which: the split is made without it)
+// with the gate in the ring (6 tensors) or not (5); the split is made without,
+// as the workspace's size must not depend on which
 NormShape norm_bwd_shape(int d, int groups, int tensors) {
-  return norm_shape(d, kBwdThreads, kBwdCtaWarps, tensors, groups > 1 ? 2 : 0);
+  return norm_shape(d, kBwdThreads, kBwdCtaVpt, kBwdCtaWarps, 160, tensors, groups > 1 ? 2 : 0);
 }
 
 NormBwdSplit norm_bwd_split(int M, int d, int rows) {
-  NormBwdSplit s;
+  NormBwdSplit s = {};
   s.rpg = rows < M ? rows : M;
   s.groups = (M + s.rpg - 1) / s.rpg;
   const NormShape sh = norm_bwd_shape(d, s.groups, 5);
   const int per_cta = sh.cta ? 1 : sh.threads / sh.lpr;
-  int most = kSms * sh.per_sm * per_cta;
-  if (!sh.cta && M <= kBwdOneCta) most = per_cta;
-  s.len = (M + most - 1) / most;
-  s.workers = (M + s.len - 1) / s.len;
-  const int ctas = most / per_cta;
-  s.ctas = s.workers < ctas ? s.workers : ctas;
+  int total = kSms * sh.per_sm * per_cta;
+  if (!sh.cta && M <= kBwdOneCta) total = per_cta;
+  s.ctas = std::min(total / per_cta, M);
+  s.spread = M <= total ? 1 : 0;
+  s.unit = 1;
+  const bool whole = s.rpg == 1 || (s.rpg <= kBwdUnit && s.groups >= total);
+  if (s.groups == 1) {
+    s.team = total;
+    s.run = M;
+  } else if (whole) {
+    // whole gate rows, no shared ones
+    s.unit = s.rpg;
+    s.team = s.spread ? 1 : per_cta * (sh.cta ? 16 : 8);
+    while (total % s.team != 0) s.team /= 2;
+    const int teams = total / s.team;
+    s.run = ((s.groups + teams - 1) / teams) * s.rpg;
+  } else if (s.spread) {
+    s.team = s.run = 1;
+  } else {
+    // the largest team whose run touches at most two gate rows
+    for (s.team = per_cta * (sh.cta ? 16 : 8);; s.team /= 2) {
+      if (total % s.team != 0) continue;
+      const int teams = total / s.team;
+      s.run = (M + teams - 1) / teams;
+      if (s.run - 1 <= s.rpg || s.team == per_cta) break;
+    }
+  }
+  s.slots = s.groups > 1 && !whole ? (s.run < 2 ? 1 : (s.run - 2) / s.rpg + 2) : 0;
   return s;
 }
 
 struct NormBwdWorkspace {
   double* alpha;  // [ctas]
   float* gain;    // [2][ctas][d]
-  float* gate;    // [workers][2][d], with several gate rows: parts of the gate rows a worker starts and ends in
+  float* gate;    // [workers][slots][d], with several gate rows: parts of the gate rows in the team's run
 };
 
 __host__ __device__ inline size_t bwd_alpha_floats(int ctas) { return 4 * static_cast<size_t>((ctas + 1) / 2); }
@@ -438,7 +469,7 @@ __device__ __forceinline__ void gain_out(const NormGateBwd& p, const NormBwdWork
 }
 
 template <int VPT, int LPR, bool CTA>
-__global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT - 1])
+__global__ void __launch_bounds__(CTA ? 256 : kBwdThreads[VPT - 1], CTA && VPT == 2 ? 2 : 1)
     norm_gate_bwd_kernel(const NormGateBwd p, const NormBwdSplit sp, const FastDiv by_rpg, const int depth,
                          const bool ring_gate, const bool direct) {
   pdl_wait();
@@ -454,8 +485,9 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
   const int t = CTA ? (tid >> 5) * (32 * VPT) + (tid & 31) : tid % LPR;
   const bool one = sp.groups == 1;
   const bool post = p.y != nullptr, pre = p.dx != nullptr;
-  // CTAs first, so that few rows spread out
-  const int me = blockIdx.x + gridDim.x * (CTA ? 0 : tid / LPR);
+  const int per_cta = CTA ? 1 : nthr / LPR;
+  const int sub = CTA ? 0 : tid / LPR;
+  const int me = sp.spread ? blockIdx.x + gridDim.x * sub : blockIdx.x * per_cta + sub;
   const float alpha = p.alpha != nullptr ? *p.alpha : 1.f;
   const uint64_t alpha2 = f2_pack(alpha, alpha);
   const float inv_d = 1.f / static_cast<float>(p.d);
@@ -473,13 +505,19 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
     for (uint32_t o = 0; o < ring_end; o += stage_bytes)
       for (int v = 0; v < 5 * VPT; ++v) *reinterpret_cast<uint4*>(mine + o + v * kVec) = zero;
   }
-  // one gate row: workers deal out the rows in turn, neighbours to neighbours;
-  // several: `len` consecutive rows each
-  const int all = gridDim.x * (CTA ? 1 : nthr / LPR);
-  const int step = one ? all : 1;
-  const int m0 = one ? min(CTA || p.M < all ? me : static_cast<int>(blockIdx.x) * (nthr / LPR) + tid / LPR, p.M)
-                     : static_cast<int>(min(static_cast<long long>(me) * sp.len, static_cast<long long>(p.M)));
-  const int m1 = one || p.M - m0 < sp.len ? p.M : m0 + sp.len;
+  // rows m0, m0 + 1, .. of a unit, then the worker's next unit, below m1
+  const int team = me / sp.team;
+  const long long r0 = static_cast<long long>(team) * sp.run;
+  const int m1 = static_cast<int>(min(r0 + sp.run, static_cast<long long>(p.M)));
+  const int m0 = static_cast<int>(min(r0 + static_cast<long long>(me - team * sp.team) * sp.unit, static_cast<long long>(m1)));
+  const int skip = min((sp.team - 1) * static_cast<long long>(sp.unit), static_cast<long long>(p.M));
+  struct Row {
+    int m, left;  // rows of the unit from m on
+  };
+  auto next = [&](Row k) {
+    if (k.left > 1) return Row{k.m + 1 < m1 ? k.m + 1 : m1, k.left - 1};
+    return Row{m1 - k.m > skip + 1 ? k.m + 1 + skip : m1, sp.unit};
+  };
   // columns of vector j: col + j * tpr * 8, in the row for j < nv
   const int col = t * 8;
   int nv = 0;
@@ -525,16 +563,15 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
     if (!one) spost[(2 * j) * nthr] = spost[(2 * j + 1) * nthr] = zero;
   }
   double salpha = 0.0;
-  const int g_first = by_rpg(m0 < p.M ? m0 : 0);
+  const int g_first = by_rpg(r0 < p.M ? static_cast<int>(r0) : 0);
   int g = -1;      // gate row of T
   int g_end = m0;  // where it ends
   // T of gate row g to its place, and its share of dw_post
   auto flush = [&]() {
-    const bool whole = g * static_cast<long long>(sp.rpg) >= m0 && g_end <= m1;
     float* dst = nullptr;
     if (p.dgate != nullptr)
-      dst = whole ? p.dgate + static_cast<size_t>(g) * p.d
-                  : ws.gate + (2 * static_cast<size_t>(me) + (g == g_first ? 0 : 1)) * p.d;
+      dst = sp.slots == 0 ? p.dgate + static_cast<size_t>(g) * p.d
+                          : ws.gate + (static_cast<size_t>(me) * sp.slots + (g - g_first)) * p.d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       uint64_t w[4], o[4], f[4];
@@ -555,19 +592,19 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
     }
   };
 
-  int m = m0, ahead = m0;
+  Row cur{m0, sp.unit}, ahead = cur;
   uint32_t off = 0, foff = (depth - 1) * stage_bytes;
-  auto next = [&](int k) { return m1 - k > step ? k + step : m1; };
-  fetch(0, ahead, qa[0], qb[0]);
+  fetch(0, ahead.m, qa[0], qb[0]);
   ahead = next(ahead);
   if (depth == 3) {
-    fetch(stage_bytes, ahead, qa[1], qb[1]);
+    fetch(stage_bytes, ahead.m, qa[1], qb[1]);
     ahead = next(ahead);
   }
   // uniform over the warp (a CTA's threads share m)
-  while (__any_sync(0xffffffffu, m < m1)) {
+  while (__any_sync(0xffffffffu, cur.m < m1)) {
+    const int m = cur.m;
     float fa, fb;
-    fetch(foff, ahead, fa, fb);
+    fetch(foff, ahead.m, fa, fb);
     ahead = next(ahead);
     const bool on = m < m1;
     if (on && m >= g_end && post) {
@@ -649,7 +686,7 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
     qb[0] = depth == 2 ? fb : qb[1];
     qa[1] = fa;
     qb[1] = fb;
-    m = next(m);
+    cur = next(cur);
     off = off + stage_bytes == ring_end ? 0 : off + stage_bytes;
     foff = foff + stage_bytes == ring_end ? 0 : foff + stage_bytes;
   }
@@ -728,15 +765,39 @@ __global__ void __launch_bounds__(CTA ? (VPT == 3 ? 352 : 256) : kBwdThreads[VPT
   }
 }
 
+__device__ __forceinline__ void add2(float2& s, const float* p) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  s.x += v.x;
+  s.y += v.y;
+}
+
+// Parts of gate row g for columns c.. that are `k0` modulo `kn` in their order.
+__device__ __forceinline__ float2 gate_parts(const NormGateBwd& p, const NormBwdSplit& sp, const float* gate, int g, int c,
+                                             int k0, int kn) {
+  const uint32_t run = sp.run, team = sp.team, rpg = sp.rpg;
+  const uint32_t r0 = g * rpg, r1 = min(r0 + rpg, static_cast<uint32_t>(p.M));
+  const uint32_t t0 = r0 / run, parts = ((r1 - 1) / run - t0 + 1) * team;
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (uint32_t i = k0; i < parts; i += kn) {
+    const uint32_t t = t0 + i / team, k = i % team;
+    const uint32_t c0 = t * run, a = max(r0, c0), b = min(r1, c0 + run);
+    // the team's worker k has rows a.. of it if the first one dealt to it is below b
+    const uint32_t behind = (a - c0) % team, row = a + (k >= behind ? k - behind : k + team - behind);
+    if (row < b) add2(s, gate + (static_cast<size_t>(t * team + k) * sp.slots + (g - c0 / rpg)) * p.d + c);
+  }
+  return s;
+}
+
 // Adds the CTAs' parts: blockIdx.y = 0, 1 the gains, 2.. gate rows that several
-// workers share.  32 columns x 32 interleaved partial sums per CTA; beyond
-// kBwdFewGroups gate rows a warp adds one gate row's few parts.
+// workers share.  64 columns x 32 interleaved partial sums per CTA; beyond
+// kBwdFewGroups gate rows a warp adds each.
 __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateBwd p, const NormBwdSplit sp) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float sh[32][33];
+  __shared__ __align__(8) float sh[32][66];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * 64 + lane * 2;
   const NormBwdWorkspace ws = bwd_workspace(p.workspace, sp.ctas, p.d);
   const int job = blockIdx.y;
   const bool one = sp.groups == 1;
@@ -748,51 +809,35 @@ __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateB
     if (lane == 0) *p.dalpha = static_cast<float>(s);
   }
   if (job >= 2 && sp.groups > kBwdFewGroups) {
-    for (int w = 1 + (job - 2) * 32 + row; w < sp.workers; w += kBwdGateJobs * 32) {
-      const int b = w * sp.len, g = b / sp.rpg;
-      const long long r0 = static_cast<long long>(g) * sp.rpg;
-      if (r0 == b || r0 / sp.len != w - 1) continue;  // not shared, or not the first worker after its owner
-      const long long r1 = min(r0 + sp.rpg, static_cast<long long>(p.M));
-      const int last = static_cast<int>((r1 - 1) / sp.len);
-      if (c >= p.d) continue;
-      float s = ws.gate[(2 * static_cast<size_t>(w - 1) + (static_cast<long long>(w - 1) * sp.len / sp.rpg == g ? 0 : 1)) * p.d + c];
-      for (int k = w; k <= last; ++k) s += ws.gate[2 * static_cast<size_t>(k) * p.d + c];
-      p.dgate[static_cast<size_t>(g) * p.d + c] = s;
-    }
+    const int g = (job - 2) * 32 + row;
+    if (g < sp.groups && c < p.d)
+      *reinterpret_cast<float2*>(p.dgate + static_cast<size_t>(g) * p.d + c) = gate_parts(p, sp, ws.gate, g, c, 0, 1);
     return;
   }
-  const float* src;
-  size_t stride = p.d;
-  int n, first = 0;  // parts, and which of the first worker's two is meant
+  float2 v = make_float2(0.f, 0.f);
   if (job < 2) {
     if (job == 0 ? p.dw_pre == nullptr : (p.dw_post == nullptr && !(one && p.dgate != nullptr))) return;
-    src = ws.gain + static_cast<size_t>(job) * sp.ctas * p.d;
-    n = sp.ctas;
-  } else {
-    const int g = job - 2;
-    const long long r0 = static_cast<long long>(g) * sp.rpg, r1 = min(r0 + sp.rpg, static_cast<long long>(p.M));
-    const int w0 = static_cast<int>(r0 / sp.len), w1 = static_cast<int>((r1 - 1) / sp.len);
-    if (w0 == w1) return;  // written by its only worker
-    src = ws.gate + 2 * static_cast<size_t>(w0) * p.d;
-    stride = 2 * static_cast<size_t>(p.d);
-    n = w1 - w0 + 1;
-    first = static_cast<long long>(w0) * sp.len / sp.rpg == g ? 0 : 1;
+    const float* src = ws.gain + static_cast<size_t>(job) * sp.ctas * p.d + c;
+    if (c < p.d) {
+#pragma unroll 4
+      for (int k = row; k < sp.ctas; k += 32) add2(v, src + static_cast<size_t>(k) * p.d);
+    }
+  } else if (c < p.d) {
+    v = gate_parts(p, sp, ws.gate, job - 2, c, row, 32);
   }
-  float s = 0.f;
-  if (c < p.d)
-    for (int k = row; k < n; k += 32) s += src[k * stride + (k == 0 ? first * static_cast<size_t>(p.d) : 0) + c];
-  sh[row][lane] = s;
+  *reinterpret_cast<float2*>(&sh[row][lane * 2]) = v;
   __syncthreads();
-  // transposed: warp `row` adds column `row`
-  s = sh[lane][row];
+  // sixteen lanes add a column
+  const int col = threadIdx.x >> 4, part = threadIdx.x & 15;
+  float s = sh[part][col] + sh[part + 16][col];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const int col = blockIdx.x * 32 + row;
-  if (lane == 0 && col < p.d) {
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int out = blockIdx.x * 64 + col;
+  if (part == 0 && out < p.d) {
     if (job < 2)
-      gain_out(p, ws, job, one, true, sp.ctas, col, s);
+      gain_out(p, ws, job, one, true, sp.ctas, out, s);
     else
-      p.dgate[static_cast<size_t>(job - 2) * p.d + col] = s;
+      p.dgate[static_cast<size_t>(job - 2) * p.d + out] = s;
   }
 }
 
@@ -840,6 +885,7 @@ template <class F>
 cudaError_t by_shape(const NormShape& s, F&& f) {
   using std::integral_constant;
   if (s.cta) {
+    if (s.vpt == 2) return f(integral_constant<int, 2>(), integral_constant<int, 32>(), std::true_type());
     if (s.vpt == 3) return f(integral_constant<int, 3>(), integral_constant<int, 32>(), std::true_type());
     return f(integral_constant<int, 4>(), integral_constant<int, 32>(), std::true_type());
   }
@@ -856,8 +902,8 @@ cudaError_t by_shape(const NormShape& s, F&& f) {
 
 cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, cudaStream_t s) {
   const bool ring_gate = p.gate != nullptr && p.rows < p.M;
-  const int threads[4] = {512, 512, 512, 512}, cta_warps[2] = {12, 12};
-  const NormShape sh = norm_shape(p.d, threads, cta_warps, ring_gate ? 3 : 2, 0);
+  const int threads[4] = {512, 512, 512, 512}, cta_vpt[2] = {3, 4}, cta_warps[2] = {12, 12};
+  const NormShape sh = norm_shape(p.d, threads, cta_vpt, cta_warps, 256, ring_gate ? 3 : 2, 0);
   return by_shape(sh, [&](auto vpt, auto lpr, auto cta) {
     return fwd_one<decltype(vpt)::value, decltype(lpr)::value, decltype(cta)::value>(p, sh, ring_gate, s);
   });
@@ -865,15 +911,16 @@ cudaError_t launch_norm_gate_fwd(const NormGateFwd& p, cudaStream_t s) {
 
 size_t norm_gate_bwd_workspace(int M, int d, int rows) {
   const NormBwdSplit sp = norm_bwd_split(M, d, rows);
-  const size_t rows_of_parts = 2 * static_cast<size_t>(sp.ctas) + (sp.groups > 1 ? 2 * static_cast<size_t>(sp.workers) : 0);
+  const size_t teams = (static_cast<size_t>(M) + sp.run - 1) / sp.run;
+  const size_t rows_of_parts = 2 * static_cast<size_t>(sp.ctas) + teams * sp.team * sp.slots;
   return (bwd_alpha_floats(sp.ctas) + rows_of_parts * d) * sizeof(float);
 }
 
 cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, cudaStream_t s) {
   const NormBwdSplit sp = norm_bwd_split(p.M, p.d, p.rows);
   // gate rows that several workers share
-  const bool gate_parts = p.dgate != nullptr && sp.groups > 1 && sp.len % sp.rpg != 0;
-  const bool direct = sp.ctas == 1 && !gate_parts;
+  const bool shared_gates = p.dgate != nullptr && sp.slots > 0;
+  const bool direct = sp.ctas == 1 && !shared_gates;
   // the gate in the ring too, where its rows are short and the ring still holds two rows of everything
   NormShape sh = norm_bwd_shape(p.d, sp.groups, 6);
   const bool ring_gate =
@@ -884,9 +931,9 @@ cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, cudaStream_t s) {
   });
   if (e != cudaSuccess || direct) return e;
   const bool one_gate = p.dgate != nullptr && sp.groups == 1;
-  if (p.dw_pre == nullptr && p.dw_post == nullptr && !one_gate && !gate_parts && p.dalpha == nullptr) return e;
-  const int jobs = 2 + (!gate_parts ? 0 : sp.groups > kBwdFewGroups ? kBwdGateJobs : sp.groups);
-  e = launch_pdl(norm_gate_bwd_sum_kernel, dim3((p.d + 31) / 32, jobs), dim3(1024), 0, s, p, sp);
+  if (p.dw_pre == nullptr && p.dw_post == nullptr && !one_gate && !shared_gates && p.dalpha == nullptr) return e;
+  const int jobs = 2 + (!shared_gates ? 0 : sp.groups > kBwdFewGroups ? (sp.groups + 31) / 32 : sp.groups);
+  e = launch_pdl(norm_gate_bwd_sum_kernel, dim3((p.d + 63) / 64, jobs), dim3(1024), 0, s, p, sp);
   count_launches(1);
   return e;
 }
