@@ -1007,10 +1007,10 @@ int check_adamw_tensors(int n, const fp8mlp_adamw_tensor* t) {
     if (t[i].n == 0) continue;
     const float* g = t[i].g;
     REQUIRE_PTR(g);
-    // chunks of 4096 elements are counted in 32 bits
+    // chunks of 2048 elements are counted in 32 bits
     if (t[i].n > (1ll << 42)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "a tensor's n is above 2^42");
-    chunks += (t[i].n + 4095) / 4096;
-    if (chunks > 0x7FFFFFFFll) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "too many elements in one call");
+    chunks += (t[i].n + 2047) / 2048;
+    if (chunks > 0x7FFF0000ll) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "too many elements in one call");
   }
   return FP8MLP_OK;
 }

@@ -28,9 +28,10 @@ namespace {
 
 using namespace dev;
 
-constexpr int kMaxTensors = 48;       // descriptors per launch (kernel arguments hold 4 KB on every driver)
-constexpr int kChunk = 4096;          // elements per CTA: 256 threads x 4 x 4
+constexpr int kFew = 32, kMany = 256;  // descriptors per launch: as kernel arguments (at most 32764 bytes)
 constexpr int kThreads = 256;
+constexpr int kStep = 8 * kThreads;  // elements a CTA takes at a time: two blocks of 128 per warp
+constexpr int kSms = 148;
 
 struct TensorArg {
   long long n;
@@ -44,10 +45,12 @@ struct TensorArg {
   float lr_mult, weight_decay;
 };
 
+template <int CAP>
 struct AdamArgs {
-  TensorArg t[kMaxTensors];
-  int first_chunk[kMaxTensors + 1];
+  TensorArg t[CAP];
+  int first_chunk[CAP + 1];
   int n_tensors;
+  int steps;    // per chunk, the CTAs' unit of work
   int tensor0;  // index of t[0] in the call (part of the random numbers)
   float beta1, beta2, om_beta1, om_beta2, eps;
   int last;  // this launch ends the call: the step count advances
@@ -78,57 +81,271 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// scaled value (|a| <= 448) -> the e4m3 value below or above it, the one above
-// with the probability of its share of the step; u in [0, 1).  a / q and the
-// multiplication back are by powers of two; q is the step of a's binade.
-__device__ __forceinline__ float e4m3_stochastic(float a, float u) {
-  const uint32_t mag = __float_as_uint(a) & 0x7FFFFFFFu;
-  const uint32_t e = max(mag >> 23, 121u);  // exponents below -6 share the subnormal step 2^-9
-  const float invq = __uint_as_float((257u - e) << 23), q = __uint_as_float((e - 3u) << 23);
-  const float k = floorf(__fadd_rn(__fmul_rn(__uint_as_float(mag), invq), u));
-  return copysignf(fminf(__fmul_rn(k, q), FP8MLP_E4M3_MAX), a);
+// Scaled value (|a| <= 448) -> the e4m3 value below or above it, the one above
+// with the probability of its share of the step: floor(|a| / q + u) q, with q
+// the step of a's binade and u in [0, 1) a multiple of 2^-16.
+//
+// From 2^-6 on, q is 2^-3 of the binade, so |a| / q + u is the mantissa with u
+// added 20 bits below the ones that stay, and a carry moves on to the next
+// binade by itself: one integer addition and a mask.
+__device__ __forceinline__ uint32_t stochastic_normal(uint32_t a, uint32_t u16_shl4) { return (a + u16_shl4) & 0xFFF00000u; }
+// Below 2^-6 the step is 2^-9.
+__device__ __noinline__ float stochastic_subnormal(float a, uint32_t u16) {
+  const float u = static_cast<float>(u16) * 0x1p-16f;
+  return copysignf(__fmul_rn(floorf(__fadd_rn(__fmul_rn(fabsf(a), 512.f), u)), 0x1p-9f), a);
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  // two codes -> two halves (exact); the upper one is unused
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xFFu)));
-  float f;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-  return f;
+// four e4m3 codes -> values (exact)
+__device__ __forceinline__ void e4m3x4_values(uint32_t codes, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(f[0]), "=f"(f[1])
+      : "r"(lo));
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(f[2]), "=f"(f[3])
+      : "r"(hi));
 }
 
+// A product that goes into a sum: as two single ones, since a packed product
+// followed by a packed sum is contracted to one rounding whatever its modifier.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  float x, y, u, v;
+  f2_unpack(a, x, y);
+  f2_unpack(b, u, v);
+  return f2_pack(__fmul_rn(x, u), __fmul_rn(y, v));
+}
+
+// Two elements' step: m, v in and out, sqrt(v) and the weight out.  A
+// difference is a sum with the factor's sign turned.
 struct StepScalars {
-  float coef, size, inv_bc2;
+  uint64_t beta1, beta2, om_beta1, om_beta2, coef, inv_bc2, eps, nsize, ndecay;
 };
+__device__ __forceinline__ uint64_t both(float x) { return f2_pack(x, x); }
 
-struct Moments {
-  float m, v;
-};
-
-__device__ __forceinline__ Moments moments(float m, float v, float g, const AdamArgs& a, float coef) {
-  const float ge = __fmul_rn(g, coef);
-  Moments r;
-  r.m = __fadd_rn(__fmul_rn(m, a.beta1), __fmul_rn(ge, a.om_beta1));
-  r.v = __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(ge, ge), a.om_beta2));
-  return r;
+__device__ __forceinline__ void step2(float (&p)[2], float (&m)[2], float (&v)[2], float (&root)[2], const float (&g)[2],
+                                      const StepScalars& c) {
+  const uint64_t ge = f2_mul(f2_pack(g[0], g[1]), c.coef);
+  f2_unpack(f2_add(mul2(f2_pack(m[0], m[1]), c.beta1), mul2(ge, c.om_beta1)), m[0], m[1]);
+  f2_unpack(f2_add(mul2(f2_pack(v[0], v[1]), c.beta2), mul2(f2_mul(ge, ge), c.om_beta2)), v[0], v[1]);
+  root[0] = __fsqrt_rn(v[0]);
+  root[1] = __fsqrt_rn(v[1]);
+  float den[2];
+  f2_unpack(f2_add(mul2(f2_pack(root[0], root[1]), c.inv_bc2), c.eps), den[0], den[1]);
+  const uint64_t q = f2_pack(__fdiv_rn(m[0], den[0]), __fdiv_rn(m[1], den[1])), w = f2_pack(p[0], p[1]);
+  f2_unpack(f2_add(f2_add(w, mul2(w, c.ndecay)), mul2(q, c.nsize)), p[0], p[1]);
 }
 
-__device__ __forceinline__ float new_weight(float p, const Moments& x, float sqrt_v, float eps, float size, float inv_bc2,
-                                            float decay) {
-  const float den = __fadd_rn(__fmul_rn(sqrt_v, inv_bc2), eps);
-  return __fsub_rn(__fsub_rn(p, __fmul_rn(p, decay)), __fmul_rn(__fdiv_rn(x.m, den), size));
-}
-
-__device__ __forceinline__ uint16_t bf16_stochastic(float x, uint32_t bits16) {
+__device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t bits16) {
   const uint32_t u = __float_as_uint(x);
-  if ((u & 0x7F800000u) == 0x7F800000u) return static_cast<uint16_t>(pack_bf16x2(x, 0.f));  // inf, NaN
-  return static_cast<uint16_t>((u + bits16) >> 16);
+  if ((u & 0x7F800000u) == 0x7F800000u) return pack_bf16x2(x, 0.f);  // inf, NaN
+  return (u + bits16) >> 16;
 }
 
-// BITS: of the moments.  A warp takes blocks of 128 elements, four per lane.
-template <int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs a) {
+// Four elements from a, or the first `valid` of them and zeros (FULL: all).
+template <bool FULL>
+__device__ __forceinline__ void load4(const float* a, int valid, float (&f)[4]) {
+  if constexpr (FULL) {
+    const float4 q = *reinterpret_cast<const float4*>(a);
+    f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = k < valid ? a[k] : 0.f;
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ void load4(const uint16_t* a, int valid, float (&f)[4]) {
+  if constexpr (FULL) {
+    const uint2 w = *reinterpret_cast<const uint2*>(a);
+    f[0] = bf16lo_to_f32(w.x), f[1] = bf16hi_to_f32(w.x), f[2] = bf16lo_to_f32(w.y), f[3] = bf16hi_to_f32(w.y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = k < valid ? bf16lo_to_f32(a[k]) : 0.f;
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ uint32_t load4(const uint8_t* a, int valid) {
+  if constexpr (FULL) return *reinterpret_cast<const uint32_t*>(a);
+  uint32_t w = 0;
+  for (int k = 0; k < valid; ++k) w |= static_cast<uint32_t>(a[k]) << (8 * k);
+  return w;
+}
+template <bool FULL>
+__device__ __forceinline__ void store4(float* a, int valid, const float (&f)[4]) {
+  if constexpr (FULL) {
+    *reinterpret_cast<float4*>(a) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < valid) a[k] = f[k];
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ void store4(uint16_t* a, int valid, uint2 w) {
+  if constexpr (FULL) {
+    *reinterpret_cast<uint2*>(a) = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < valid) a[k] = static_cast<uint16_t>((k < 2 ? w.x : w.y) >> (16 * (k & 1)));
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ void store4(uint8_t* a, int valid, uint32_t w) {
+  if constexpr (FULL) {
+    *reinterpret_cast<uint32_t*>(a) = w;
+  } else {
+    for (int k = 0; k < valid; ++k) a[k] = static_cast<uint8_t>(w >> (8 * k));
+  }
+}
+
+// One warp, 256 elements from `base` on (fewer without FULL).
+template <int BITS, bool FULL>
+__device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars& sc, long long base, int lane, uint32_t key) {
+  const long long i = base + lane * 4;  // and + 128
+  int valid[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const long long left = t.n - i - b * 128;
+    valid[b] = FULL || left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
+  }
+  float g[2][4], p[2][4], m[2][4], v[2][4], root[2][4];
+  uint32_t cm[2], cv[2];
+  const float* gp = t.g + i;
+  float* pp = t.p + i;
+  uint16_t* p16 = t.p_bf16 + i;
+  float *m32 = static_cast<float*>(t.m) + i, *v32 = static_cast<float*>(t.v) + i;
+  uint8_t *m8 = static_cast<uint8_t*>(t.m) + i, *v8 = static_cast<uint8_t*>(t.v) + i;
+  const long long blk = base >> 7;
+  float sm[2], sv[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    load4<FULL>(gp + b * 128, valid[b], g[b]);
+    if (t.p != nullptr)
+      load4<FULL>(pp + b * 128, valid[b], p[b]);
+    else
+      load4<FULL>(p16 + b * 128, valid[b], p[b]);
+    if constexpr (BITS == 32) {
+      load4<FULL>(m32 + b * 128, valid[b], m[b]);
+      load4<FULL>(v32 + b * 128, valid[b], v[b]);
+    } else {
+      cm[b] = load4<FULL>(m8 + b * 128, valid[b]);
+      cv[b] = load4<FULL>(v8 + b * 128, valid[b]);
+      const bool in = FULL || (blk + b) * 128 < t.n;
+      sm[b] = in ? t.m_scale[blk + b] : 0.f;
+      sv[b] = in ? t.v_scale[blk + b] : 0.f;
+    }
+  }
+  uint32_t bits[2][4];
+  if (BITS == 8 || t.p == nullptr) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bits[b][k] = mix32(mix32(static_cast<uint32_t>(i + b * 128 + k) ^ key) + key);
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    if constexpr (BITS == 8) {
+      e4m3x4_values(cm[b], m[b]);
+      e4m3x4_values(cv[b], v[b]);
+      const uint64_t s1 = both(sm[b]), s2 = both(sv[b]);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        f2_unpack(f2_mul(f2_pack(m[b][k], m[b][k + 1]), s1), m[b][k], m[b][k + 1]);
+        const uint64_t u = f2_mul(f2_pack(v[b][k], v[b][k + 1]), s2);
+        f2_unpack(f2_mul(u, u), v[b][k], v[b][k + 1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      float tp[2] = {p[b][k], p[b][k + 1]}, tm[2] = {m[b][k], m[b][k + 1]}, tv[2] = {v[b][k], v[b][k + 1]}, tr[2];
+      const float tg[2] = {g[b][k], g[b][k + 1]};
+      step2(tp, tm, tv, tr, tg, sc);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        p[b][k + j] = tp[j];
+        m[b][k + j] = tm[j];
+        v[b][k + j] = tv[j];
+        root[b][k + j] = tr[j];
+      }
+    }
+    if (t.p != nullptr) {
+      store4<FULL>(pp + b * 128, valid[b], p[b]);
+      if (t.p_bf16 != nullptr)
+        store4<FULL>(p16 + b * 128, valid[b], make_uint2(pack_bf16x2(p[b][0], p[b][1]), pack_bf16x2(p[b][2], p[b][3])));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = bf16_stochastic(p[b][k], mix32(bits[b][k] ^ 0x5BD1E995u) & 0xFFFFu);
+      store4<FULL>(p16 + b * 128, valid[b], make_uint2((w[0] & 0xFFFFu) | (w[1] << 16), (w[2] & 0xFFFFu) | (w[3] << 16)));
+    }
+    if constexpr (BITS == 32) {
+      store4<FULL>(m32 + b * 128, valid[b], m[b]);
+      store4<FULL>(v32 + b * 128, valid[b], v[b]);
+    }
+  }
+  if constexpr (BITS == 8) {
+    // block maxima, as integers: magnitudes order like their bits, NaN above
+    // infinity; elements past the end are zero
+    uint32_t top[4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t am = 0, av = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        am = max(am, __float_as_uint(m[b][k]) & 0x7FFFFFFFu);
+        av = max(av, __float_as_uint(root[b][k]) & 0x7FFFFFFFu);
+      }
+      top[b] = __reduce_max_sync(0xffffffffu, am);
+      top[2 + b] = __reduce_max_sync(0xffffffffu, av);
+    }
+    const int q = lane >> 3;  // m of block 0 and 1, v of block 0 and 1
+    float inv;
+    const float s = block_scale(__uint_as_float(q == 0 ? top[0] : q == 1 ? top[1] : q == 2 ? top[2] : top[3]), &inv);
+    if ((lane & 7) == 0 && (FULL || (blk + (q & 1)) * 128 < t.n)) (q < 2 ? t.m_scale : t.v_scale)[blk + (q & 1)] = inv;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float s1 = __shfl_sync(0xffffffffu, s, b * 8), s2 = __shfl_sync(0xffffffffu, s, 16 + b * 8);
+      const uint64_t s1x2 = both(s1), s2x2 = both(s2);
+      float em[4], ev[4], qm[4], qv[4];
+      uint32_t low = 0xFFFFFFFFu;  // smallest magnitude above zero, less one unit
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        f2_unpack(f2_mul(f2_pack(m[b][k], m[b][k + 1]), s1x2), em[k], em[k + 1]);
+        f2_unpack(f2_mul(f2_pack(root[b][k], root[b][k + 1]), s2x2), ev[k], ev[k + 1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = bits[b][k];
+        qm[k] = __uint_as_float(stochastic_normal(__float_as_uint(em[k]), (w << 4) & 0xFFFF0u));
+        qv[k] = __uint_as_float(stochastic_normal(__float_as_uint(ev[k]), (w >> 12) & 0xFFFF0u));
+        low = min(low, min((__float_as_uint(em[k]) & 0x7FFFFFFFu) - 1u, __float_as_uint(ev[k]) - 1u));
+      }
+      // magnitudes below 2^-6 are rare; a positive sqrt(v) so far below its
+      // block's largest that the product is zero needs a scale under 2^-54
+      if (low < 0x3C800000u - 1u || s2 < 0x1p-50f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = bits[b][k];
+          if (fabsf(em[k]) < 0x1p-6f && em[k] != 0.f) qm[k] = stochastic_subnormal(em[k], w & 0xFFFFu);
+          if (ev[k] < 0x1p-6f && root[b][k] > 0.f) qv[k] = fmaxf(stochastic_subnormal(ev[k], w >> 16), 0x1p-9f);
+        }
+      }
+      store4<FULL>(m8 + b * 128, valid[b], pack_e4m3x2(qm[0], qm[1]) | (pack_e4m3x2(qm[2], qm[3]) << 16));
+      store4<FULL>(v8 + b * 128, valid[b], pack_e4m3x2(qv[0], qv[1]) | (pack_e4m3x2(qv[2], qv[3]) << 16));
+    }
+  }
+}
+
+// BITS: of the moments.  CTAs are persistent (the powers of beta take as long
+// as a chunk).  A warp takes two blocks of 128 elements at a time, four
+// elements of each per lane; its four block maxima take one integer reduction
+// each, and a quarter of the warp works out each block's scale.
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ double corr[2];
@@ -147,156 +364,37 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
   __syncthreads();
   const bool skip = !(fabsf(coef) <= 3.4028234664e38f);  // a NaN or infinite coefficient: the step is not taken
-  if (!skip) {
-    const int ti = find_tensor(a, blockIdx.x);
+  const int chunks = skip ? 0 : a.first_chunk[a.n_tensors];
+  StepScalars sc;
+  sc.beta1 = both(a.beta1);
+  sc.beta2 = both(a.beta2);
+  sc.om_beta1 = both(a.om_beta1);
+  sc.om_beta2 = both(a.om_beta2);
+  sc.coef = both(coef);
+  sc.inv_bc2 = both(static_cast<float>(1.0 / sqrt(corr[1])));
+  sc.eps = both(a.eps);
+  sc.nsize = sc.ndecay = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int known = -1;  // tensor that sc's last two and the key belong to
+  uint32_t key = 0;
+  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const int ti = find_tensor(a, chunk);
     const TensorArg& t = a.t[ti];
-    const float lr_t = __fmul_rn(lr, t.lr_mult);
-    const float size = static_cast<float>(static_cast<double>(lr_t) / corr[0]);
-    const float inv_bc2 = static_cast<float>(1.0 / sqrt(corr[1]));
-    const float decay = __fmul_rn(lr_t, t.weight_decay);
-    const uint32_t key = mix32(static_cast<uint32_t>(a.tensor0 + ti) * 0x9E3779B9u +
-                               static_cast<uint32_t>(step) * 0x7F4A7C15u + seed);
-    const long long base = static_cast<long long>(blockIdx.x - a.first_chunk[ti]) * kChunk;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 2
-    for (int it = 0; it < kChunk / 1024; ++it) {
-      const long long i0 = base + it * 1024 + warp * 128 + lane * 4;
-      if (i0 - lane * 4 >= t.n) break;  // the whole warp is past the end
-      const int valid = t.n - i0 >= 4 ? 4 : (t.n > i0 ? static_cast<int>(t.n - i0) : 0);
-      const bool full = valid == 4;
-      float g[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f};
-      Moments x[4];
-      float m[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-      const long long blk = i0 >> 7;
-      if (full) {
-        const float4 q = *reinterpret_cast<const float4*>(t.g + i0);
-        g[0] = q.x, g[1] = q.y, g[2] = q.z, g[3] = q.w;
-        if (t.p != nullptr) {
-          const float4 w = *reinterpret_cast<const float4*>(t.p + i0);
-          p[0] = w.x, p[1] = w.y, p[2] = w.z, p[3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(t.p_bf16 + i0);
-          p[0] = bf16lo_to_f32(w.x), p[1] = bf16hi_to_f32(w.x), p[2] = bf16lo_to_f32(w.y), p[3] = bf16hi_to_f32(w.y);
-        }
-        if constexpr (BITS == 32) {
-          const float4 a4 = *reinterpret_cast<const float4*>(static_cast<const float*>(t.m) + i0);
-          const float4 b4 = *reinterpret_cast<const float4*>(static_cast<const float*>(t.v) + i0);
-          m[0] = a4.x, m[1] = a4.y, m[2] = a4.z, m[3] = a4.w;
-          v[0] = b4.x, v[1] = b4.y, v[2] = b4.z, v[3] = b4.w;
-        } else {
-          const uint32_t cm = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i0);
-          const uint32_t cv = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            m[k] = e4m3_value(cm >> (8 * k));
-            v[k] = e4m3_value(cv >> (8 * k));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < valid) {
-            g[k] = t.g[i0 + k];
-            p[k] = t.p != nullptr ? t.p[i0 + k] : bf16lo_to_f32(t.p_bf16[i0 + k]);
-            if constexpr (BITS == 32) {
-              m[k] = static_cast<const float*>(t.m)[i0 + k];
-              v[k] = static_cast<const float*>(t.v)[i0 + k];
-            } else {
-              m[k] = e4m3_value(static_cast<const uint8_t*>(t.m)[i0 + k]);
-              v[k] = e4m3_value(static_cast<const uint8_t*>(t.v)[i0 + k]);
-            }
-          }
-        }
-      }
-      if constexpr (BITS == 8) {
-        const float sm = t.m_scale[blk], sv = t.v_scale[blk];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m[k] = __fmul_rn(m[k], sm);
-          v[k] = __fmul_rn(v[k], sv);
-          v[k] = __fmul_rn(v[k], v[k]);
-        }
-      }
-      float root[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[k] = moments(m[k], v[k], g[k], a, coef);
-        root[k] = __fsqrt_rn(x[k].v);
-        p[k] = new_weight(p[k], x[k], root[k], a.eps, size, inv_bc2, decay);
-      }
-      uint32_t bits[4];
-      if (BITS == 8 || t.p == nullptr) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) bits[k] = mix32(mix32(static_cast<uint32_t>(i0 + k) ^ key) + key);
-      }
-      uint16_t w16[4];
-      if (t.p != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w16[k] = static_cast<uint16_t>(pack_bf16x2(p[k], 0.f));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w16[k] = bf16_stochastic(p[k], mix32(bits[k] ^ 0x5BD1E995u) & 0xFFFFu);
-      }
-      uint32_t cm = 0, cv = 0;
-      if constexpr (BITS == 8) {
-        float am = 0.f, av = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < valid) {
-            am = max_nan(am, fabsf(x[k].m));
-            av = max_nan(av, root[k]);
-          }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
-          av = max_nan(av, __shfl_xor_sync(0xffffffffu, av, o));
-        }
-        float im, iv;
-        const float sm = block_scale(am, &im), sv = block_scale(av, &iv);
-        if (lane == 0) {
-          t.m_scale[blk] = im;
-          t.v_scale[blk] = iv;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float um = static_cast<float>(bits[k] & 0xFFFFu) * 0x1p-16f, uv = static_cast<float>(bits[k] >> 16) * 0x1p-16f;
-          const float em = fminf(fmaxf(__fmul_rn(x[k].m, sm), -FP8MLP_E4M3_MAX), FP8MLP_E4M3_MAX);
-          const float ev = fminf(__fmul_rn(root[k], sv), FP8MLP_E4M3_MAX);
-          float qm = e4m3_stochastic(em, um), qv = e4m3_stochastic(ev, uv);
-          if (root[k] > 0.f && qv == 0.f) qv = 0x1p-9f;
-          cm |= (pack_e4m3x2(qm, 0.f) & 0xFFu) << (8 * k);
-          cv |= (pack_e4m3x2(qv, 0.f) & 0xFFu) << (8 * k);
-        }
-      }
-      if (full) {
-        if (t.p != nullptr) *reinterpret_cast<float4*>(t.p + i0) = make_float4(p[0], p[1], p[2], p[3]);
-        if (t.p_bf16 != nullptr)
-          *reinterpret_cast<uint2*>(t.p_bf16 + i0) =
-              make_uint2(w16[0] | (static_cast<uint32_t>(w16[1]) << 16), w16[2] | (static_cast<uint32_t>(w16[3]) << 16));
-        if constexpr (BITS == 32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(t.m) + i0) = make_float4(x[0].m, x[1].m, x[2].m, x[3].m);
-          *reinterpret_cast<float4*>(static_cast<float*>(t.v) + i0) = make_float4(x[0].v, x[1].v, x[2].v, x[3].v);
-        } else {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i0) = cm;
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i0) = cv;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < valid) {
-            if (t.p != nullptr) t.p[i0 + k] = p[k];
-            if (t.p_bf16 != nullptr) t.p_bf16[i0 + k] = w16[k];
-            if constexpr (BITS == 32) {
-              static_cast<float*>(t.m)[i0 + k] = x[k].m;
-              static_cast<float*>(t.v)[i0 + k] = x[k].v;
-            } else {
-              static_cast<uint8_t*>(t.m)[i0 + k] = static_cast<uint8_t>(cm >> (8 * k));
-              static_cast<uint8_t*>(t.v)[i0 + k] = static_cast<uint8_t>(cv >> (8 * k));
-            }
-          }
-        }
-      }
+    if (ti != known) {
+      const float lr_t = __fmul_rn(lr, t.lr_mult);
+      sc.nsize = both(-static_cast<float>(static_cast<double>(lr_t) / corr[0]));
+      sc.ndecay = both(-__fmul_rn(lr_t, t.weight_decay));
+      key = mix32(static_cast<uint32_t>(a.tensor0 + ti) * 0x9E3779B9u + static_cast<uint32_t>(step) * 0x7F4A7C15u + seed);
+      known = ti;
+    }
+    long long base = (static_cast<long long>(chunk - a.first_chunk[ti]) * a.steps * 8 + warp) * 256;
+#pragma unroll 1
+    for (int k = 0; k < a.steps; ++k, base += kStep) {
+      if (base >= t.n) break;
+      if (base + 256 <= t.n)
+        warp_step<BITS, true>(t, sc, base, lane, key);
+      else
+        warp_step<BITS, false>(t, sc, base, lane, key);
     }
   }
   if (!a.last) return;
@@ -354,17 +452,24 @@ __global__ void __launch_bounds__(kThreads) grad_sq_kernel(const __grid_constant
   const long long n = a.n[ti];
   const long long base = static_cast<long long>(blockIdx.x - a.first_chunk[ti]) * kNormChunk;
   double s0 = 0.0, s1 = 0.0;
-#pragma unroll 4
-  for (int it = 0; it < kNormChunk / (4 * kThreads); ++it) {
-    const long long i = base + (it * kThreads + threadIdx.x) * 4;
-    if (i + 4 <= n) {
-      const float4 v = *reinterpret_cast<const float4*>(g + i);
-      s0 = fma(static_cast<double>(v.x), static_cast<double>(v.x), s0);
-      s1 = fma(static_cast<double>(v.y), static_cast<double>(v.y), s1);
-      s0 = fma(static_cast<double>(v.z), static_cast<double>(v.z), s0);
-      s1 = fma(static_cast<double>(v.w), static_cast<double>(v.w), s1);
+#pragma unroll 1
+  for (int it = 0; it < kNormChunk / (4 * kThreads); it += 8) {
+    const long long i0 = base + (it * kThreads + threadIdx.x) * 4;
+    if (i0 + 28 * kThreads + 4 <= n) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const float4*>(g + i0 + 4 * kThreads * k);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s0 = fma(static_cast<double>(v[k].x), static_cast<double>(v[k].x), s0);
+        s1 = fma(static_cast<double>(v[k].y), static_cast<double>(v[k].y), s1);
+        s0 = fma(static_cast<double>(v[k].z), static_cast<double>(v[k].z), s0);
+        s1 = fma(static_cast<double>(v[k].w), static_cast<double>(v[k].w), s1);
+      }
     } else {
-      for (long long k = i; k < n; ++k) s0 = fma(static_cast<double>(g[k]), static_cast<double>(g[k]), s0);
+      for (int k = 0; k < 8; ++k)
+        for (long long i = i0 + 4 * kThreads * k, e = i + 4; i < e && i < n; ++i)
+          s0 = fma(static_cast<double>(g[i]), static_cast<double>(g[i]), s0);
     }
   }
   double s = s0 + s1;
@@ -399,6 +504,60 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(const double* part, lon
 }
 
 long long chunks_of(long long n, int chunk) { return (n + chunk - 1) / chunk; }
+
+template <int CAP>
+cudaError_t launch_adamw_cap(int n, const fp8mlp_adamw_tensor* t, fp8mlp_adamw_state* st, int state_bits, float beta1,
+                             float beta2, float eps, const float* grad_coef, unsigned int* status, cudaStream_t s) {
+  AdamArgs<CAP> a;
+  a.beta1 = beta1;
+  a.beta2 = beta2;
+  a.om_beta1 = static_cast<float>(1.0 - static_cast<double>(beta1));
+  a.om_beta2 = static_cast<float>(1.0 - static_cast<double>(beta2));
+  a.eps = eps;
+  a.st = st;
+  a.coef = grad_coef;
+  a.status = status;
+  int last = -1;  // the last tensor with elements
+  long long all = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n > 0) last = i;
+    all += t[i].n;
+  }
+  // chunks of up to eight steps, as long as every CTA gets four of them
+  const int most = kSms * 3;
+  const long long fit = all / (static_cast<long long>(kStep) * most * 4);
+  a.steps = fit < 1 ? 1 : fit > 8 ? 8 : static_cast<int>(fit);
+  for (int i = 0; i <= last;) {
+    a.n_tensors = 0;
+    a.first_chunk[0] = 0;
+    a.tensor0 = i;
+    // consecutive tensors: the random numbers go by a tensor's place in the call
+    for (; i <= last && a.n_tensors < CAP; ++i) {
+      TensorArg& d = a.t[a.n_tensors];
+      d.n = t[i].n;
+      d.p = t[i].p;
+      d.p_bf16 = t[i].p_bf16;
+      d.g = t[i].g;
+      d.m = t[i].m;
+      d.v = t[i].v;
+      d.m_scale = t[i].m_scale;
+      d.v_scale = t[i].v_scale;
+      d.lr_mult = t[i].lr_mult;
+      d.weight_decay = t[i].weight_decay;
+      a.first_chunk[a.n_tensors + 1] = a.first_chunk[a.n_tensors] + static_cast<int>(chunks_of(t[i].n, a.steps * kStep));
+      ++a.n_tensors;
+    }
+    a.last = i > last;
+    const int chunks = a.first_chunk[a.n_tensors];
+    if (chunks == 0) continue;  // only empty tensors, and more to come
+    const dim3 grid(chunks < most ? chunks : most);
+    const cudaError_t e = state_bits == 32 ? launch_pdl(adamw_kernel<32, CAP>, grid, dim3(kThreads), 0, s, a)
+                                           : launch_pdl(adamw_kernel<8, CAP>, grid, dim3(kThreads), 0, s, a);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace
 
@@ -447,47 +606,8 @@ cudaError_t launch_grad_norm(int n, const fp8mlp_adamw_tensor* t, float max_norm
 
 cudaError_t launch_adamw(int n, const fp8mlp_adamw_tensor* t, fp8mlp_adamw_state* st, int state_bits, float beta1,
                          float beta2, float eps, const float* grad_coef, unsigned int* status, cudaStream_t s) {
-  AdamArgs a;
-  a.beta1 = beta1;
-  a.beta2 = beta2;
-  a.om_beta1 = static_cast<float>(1.0 - static_cast<double>(beta1));
-  a.om_beta2 = static_cast<float>(1.0 - static_cast<double>(beta2));
-  a.eps = eps;
-  a.st = st;
-  a.coef = grad_coef;
-  a.status = status;
-  int last = -1;  // the last tensor with elements
-  for (int i = 0; i < n; ++i)
-    if (t[i].n > 0) last = i;
-  for (int i = 0; i <= last;) {
-    a.n_tensors = 0;
-    a.first_chunk[0] = 0;
-    a.tensor0 = i;
-    // consecutive tensors: the random numbers go by a tensor's place in the call
-    for (; i <= last && a.n_tensors < kMaxTensors; ++i) {
-      TensorArg& d = a.t[a.n_tensors];
-      d.n = t[i].n;
-      d.p = t[i].p;
-      d.p_bf16 = t[i].p_bf16;
-      d.g = t[i].g;
-      d.m = t[i].m;
-      d.v = t[i].v;
-      d.m_scale = t[i].m_scale;
-      d.v_scale = t[i].v_scale;
-      d.lr_mult = t[i].lr_mult;
-      d.weight_decay = t[i].weight_decay;
-      a.first_chunk[a.n_tensors + 1] = a.first_chunk[a.n_tensors] + static_cast<int>(chunks_of(t[i].n, kChunk));
-      ++a.n_tensors;
-    }
-    a.last = i > last;
-    const int grid = a.first_chunk[a.n_tensors];
-    if (grid == 0) continue;  // only empty tensors, and more to come
-    const cudaError_t e = state_bits == 32 ? launch_pdl(adamw_kernel<32>, dim3(grid), dim3(kThreads), 0, s, a)
-                                           : launch_pdl(adamw_kernel<8>, dim3(grid), dim3(kThreads), 0, s, a);
-    count_launches(1);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return n <= kFew ? launch_adamw_cap<kFew>(n, t, st, state_bits, beta1, beta2, eps, grad_coef, status, s)
+                   : launch_adamw_cap<kMany>(n, t, st, state_bits, beta1, beta2, eps, grad_coef, status, s);
 }
 
 }  // namespace fp8mlp

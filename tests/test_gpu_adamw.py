@@ -106,12 +106,12 @@ def test_step_is_the_fp32_step(bits, master, copy):
 
 @pytest.mark.parametrize("bits", [32, 8])
 def test_more_tensors_than_one_launch_takes(bits):
-    sizes = [(37 * i) % 900 for i in range(131)]  # empty ones among them
+    sizes = [(37 * i) % 900 for i in range(300)]  # empty ones among them
     ts = tensors(sizes, bits, True)
     opt, raws = build(ts, bits, True)
     n0 = A.fp8mlp_kernel_launch_count()
     opt.step()
-    assert A.fp8mlp_kernel_launch_count() - n0 == 3
+    assert A.fp8mlp_kernel_launch_count() - n0 == 2
     torch.cuda.synchronize()
     assert opt.read_state()["step"] == 5
     for i, (t, e) in enumerate(zip(ts, opt.entries)):
