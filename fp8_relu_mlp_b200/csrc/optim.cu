@@ -88,11 +88,14 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
 // From 2^-6 on, q is 2^-3 of the binade, so |a| / q + u is the mantissa with u
 // added 20 bits below the ones that stay, and a carry moves on to the next
 // binade by itself: one integer addition and a mask.
-__device__ __forceinline__ uint32_t stochastic_normal(uint32_t a, uint32_t u16_shl4) { return (a + u16_shl4) & 0xFFF00000u; }
+__device__ __forceinline__ float stochastic_normal(float a, uint32_t u16) {
+  return __uint_as_float((__float_as_uint(a) + (u16 << 4)) & 0xFFF00000u);
+}
 // Below 2^-6 the step is 2^-9.
-__device__ __noinline__ float stochastic_subnormal(float a, uint32_t u16) {
-  const float u = static_cast<float>(u16) * 0x1p-16f;
-  return copysignf(__fmul_rn(floorf(__fadd_rn(__fmul_rn(fabsf(a), 512.f), u)), 0x1p-9f), a);
+__device__ __forceinline__ float stochastic_subnormal(float a, uint32_t u16) {
+  const float u = __uint_as_float(0x3F800000u + (u16 << 7)) - 1.f;  // u16 2^-16
+  const float k = __fadd_rd(__fmaf_rn(fabsf(a), 512.f, u), 0x1p23f) - 0x1p23f;  // floor
+  return copysignf(k * 0x1p-9f, a);
 }
 
 // four e4m3 codes -> values (exact)
@@ -140,9 +143,7 @@ __device__ __forceinline__ void step2(float (&p)[2], float (&m)[2], float (&v)[2
 }
 
 __device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t bits16) {
-  const uint32_t u = __float_as_uint(x);
-  if ((u & 0x7F800000u) == 0x7F800000u) return pack_bf16x2(x, 0.f);  // inf, NaN
-  return (u + bits16) >> 16;
+  return x == x ? (__float_as_uint(x) + bits16) >> 16 : 0x7FFFu;  // an infinity keeps its exponent
 }
 
 // Four elements from a, or the first `valid` of them and zeros (FULL: all).
@@ -244,7 +245,10 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) bits[b][k] = mix32(mix32(static_cast<uint32_t>(i + b * 128 + k) ^ key) + key);
+      for (int k = 0; k < 4; ++k) {
+        bits[b][k] = mix32(mix32(static_cast<uint32_t>(i + b * 128 + k) ^ key) + key);
+        asm volatile("" : "+r"(bits[b][k]));  // once: the compiler would compute them again for each use
+      }
   }
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -293,14 +297,10 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
     uint32_t top[4];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      uint32_t am = 0, av = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        am = max(am, __float_as_uint(m[b][k]) & 0x7FFFFFFFu);
-        av = max(av, __float_as_uint(root[b][k]) & 0x7FFFFFFFu);
-      }
-      top[b] = __reduce_max_sync(0xffffffffu, am);
-      top[2 + b] = __reduce_max_sync(0xffffffffu, av);
+      const float am = max3_nan(max_nan(fabsf(m[b][0]), fabsf(m[b][1])), fabsf(m[b][2]), fabsf(m[b][3]));
+      const float av = max3_nan(max_nan(root[b][0], root[b][1]), root[b][2], root[b][3]);
+      top[b] = __reduce_max_sync(0xffffffffu, __float_as_uint(am) & 0x7FFFFFFFu);
+      top[2 + b] = __reduce_max_sync(0xffffffffu, __float_as_uint(av) & 0x7FFFFFFFu);
     }
     const int q = lane >> 3;  // m of block 0 and 1, v of block 0 and 1
     float inv;
@@ -311,7 +311,7 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
       const float s1 = __shfl_sync(0xffffffffu, s, b * 8), s2 = __shfl_sync(0xffffffffu, s, 16 + b * 8);
       const uint64_t s1x2 = both(s1), s2x2 = both(s2);
       float em[4], ev[4], qm[4], qv[4];
-      uint32_t low = 0xFFFFFFFFu;  // smallest magnitude above zero, less one unit
+      uint32_t low = 0xFFFFFFFFu;  // bits of the smallest magnitude above zero, twice, less one
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         f2_unpack(f2_mul(f2_pack(m[b][k], m[b][k + 1]), s1x2), em[k], em[k + 1]);
@@ -320,18 +320,19 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t w = bits[b][k];
-        qm[k] = __uint_as_float(stochastic_normal(__float_as_uint(em[k]), (w << 4) & 0xFFFF0u));
-        qv[k] = __uint_as_float(stochastic_normal(__float_as_uint(ev[k]), (w >> 12) & 0xFFFF0u));
-        low = min(low, min((__float_as_uint(em[k]) & 0x7FFFFFFFu) - 1u, __float_as_uint(ev[k]) - 1u));
+        qm[k] = stochastic_normal(em[k], w & 0xFFFFu);
+        qv[k] = stochastic_normal(ev[k], w >> 16);
+        low = min(low, min(2u * __float_as_uint(em[k]) - 1u, 2u * __float_as_uint(ev[k]) - 1u));
       }
       // magnitudes below 2^-6 are rare; a positive sqrt(v) so far below its
       // block's largest that the product is zero needs a scale under 2^-54
-      if (low < 0x3C800000u - 1u || s2 < 0x1p-50f) {
+      if (low < 2u * 0x3C800000u - 1u || s2 < 0x1p-50f) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t w = bits[b][k];
-          if (fabsf(em[k]) < 0x1p-6f && em[k] != 0.f) qm[k] = stochastic_subnormal(em[k], w & 0xFFFFu);
-          if (ev[k] < 0x1p-6f && root[b][k] > 0.f) qv[k] = fmaxf(stochastic_subnormal(ev[k], w >> 16), 0x1p-9f);
+          const float sub_m = stochastic_subnormal(em[k], w & 0xFFFFu), sub_v = stochastic_subnormal(ev[k], w >> 16);
+          qm[k] = fabsf(em[k]) < 0x1p-6f ? sub_m : qm[k];
+          qv[k] = ev[k] < 0x1p-6f ? (root[b][k] > 0.f ? fmaxf(sub_v, 0x1p-9f) : 0.f) : qv[k];
         }
       }
       store4<FULL>(m8 + b * 128, valid[b], pack_e4m3x2(qm[0], qm[1]) | (pack_e4m3x2(qm[2], qm[3]) << 16));
@@ -345,7 +346,7 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
 // elements of each per lane; its four block maxima take one integer reduction
 // each, and a quarter of the warp works out each block's scale.
 template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamArgs<CAP> a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ double corr[2];
@@ -524,7 +525,7 @@ cudaError_t launch_adamw_cap(int n, const fp8mlp_adamw_tensor* t, fp8mlp_adamw_s
     all += t[i].n;
   }
   // chunks of up to eight steps, as long as every CTA gets four of them
-  const int most = kSms * 3;
+  const int most = kSms * (state_bits == 8 ? 4 : 3);
   const long long fit = all / (static_cast<long long>(kStep) * most * 4);
   a.steps = fit < 1 ? 1 : fit > 8 ? 8 : static_cast<int>(fit);
   for (int i = 0; i <= last;) {
