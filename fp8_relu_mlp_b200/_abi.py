@@ -147,12 +147,37 @@ def _ptr(t):
     raise TypeError(f"cannot pass {type(t)} as a pointer")
 
 
+_current = None  # () -> (device index, raw stream of the current stream); set once a GPU has been seen
+
+
+def _find_current():
+    """Sets ``_current``.  torch's own accessors build a Stream object per call
+    and ask again whether there is a GPU, several microseconds; the ones below
+    them are taken where this torch has them."""
+    global _current
+    import torch
+    if not torch.cuda.is_available():
+        return False
+    torch.cuda.current_stream()  # initialises the context
+    get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def fast():
+        d = get_device()
+        return d, raw(d)
+
+    def plain():
+        return torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+
+    _current = plain if raw is None else fast
+    return True
+
+
 def _stream(s):
     if s is None:
         try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
+            if _current is not None or _find_current():
+                return _current()[1]
         except Exception:
             pass
         return None
@@ -161,8 +186,14 @@ def _stream(s):
     return s.cuda_stream
 
 
+_functions = {}
+
+
 def _call(name, *args):
-    rc = getattr(lib, name)(*args)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib, name)
+    rc = fn(*args)
     if rc != OK:
         raise Fp8MlpError(rc, name)
     return rc
@@ -358,23 +389,42 @@ def fp8mlp_residual_add(M, d, r, out, r_next, stream=None):
 # handed a short buffer, or one of another GPU, would write out of bounds.
 # ---------------------------------------------------------------------------
 
-def _buf(t, need, name):
-    """Device address of ``t`` with at least ``need`` bytes (None stays NULL;
-    an int is an address the caller vouches for)."""
-    if t is None or isinstance(t, int):
+def _here(stream):
+    """Current device (None without a GPU) and the raw stream of a call."""
+    dev, raw = (_current or _no_gpu)()
+    if stream is None:
+        return dev, raw
+    return dev, stream if stream.__class__ is int else stream.cuda_stream
+
+
+def _buf(t, need, name, dev):
+    """Device address of ``t`` with at least ``need`` bytes on device ``dev``
+    (None stays NULL; an int is an address the caller vouches for)."""
+    if t is None or t.__class__ is int:
         return t
-    if not hasattr(t, "data_ptr"):
-        raise TypeError(f"{name}: cannot pass {type(t)} as a pointer")
+    try:
+        ok = t.is_contiguous() and t.nbytes >= need and t.get_device() == dev
+    except AttributeError:
+        raise TypeError(f"{name}: cannot pass {type(t)} as a pointer") from None
+    if not ok:
+        _refuse(t, need, name, dev)
+    return t.data_ptr()
+
+
+def _no_gpu():
+    """Stands in for ``_current`` until a GPU has been seen."""
+    return _current() if _find_current() else (None, None)
+
+
+def _refuse(t, need, name, dev):
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor arguments must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is needed")
-    import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
     if t.nbytes < need:
         raise ValueError(f"{name}: {need} bytes are needed, the tensor has {t.nbytes}")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
 
 
 def _kblocks(n):
@@ -382,44 +432,50 @@ def _kblocks(n):
 
 
 def fp8mlp_quantize_block(M, K, x, xq, xs, stream=None):
-    return _call("fp8mlp_quantize_block", M, K, _buf(x, 2 * M * K, "x"), _buf(xq, M * K, "xq"),
-                 _buf(xs, 4 * M * _kblocks(K), "xs"), _stream(stream))
+    dev, raw = _here(stream)
+    return _call("fp8mlp_quantize_block", M, K, _buf(x, 2 * M * K, "x", dev), _buf(xq, M * K, "xq", dev),
+                 _buf(xs, 4 * M * _kblocks(K), "xs", dev), raw)
 
 
 def fp8mlp_weight_block_cache_refresh(N, K, W, Wq, ws, Wq_t=None, ws_t=None, stream=None):
+    dev, raw = _here(stream)
     sc = 4 * _kblocks(K) * _kblocks(N)
-    return _call("fp8mlp_weight_block_cache_refresh", N, K, _buf(W, 2 * N * K, "W"), _buf(Wq, N * K, "Wq"),
-                 _buf(ws, sc, "ws"), _buf(Wq_t, N * K, "Wq_t"), _buf(ws_t, sc, "ws_t"), _stream(stream))
+    return _call("fp8mlp_weight_block_cache_refresh", N, K, _buf(W, 2 * N * K, "W", dev), _buf(Wq, N * K, "Wq", dev),
+                 _buf(ws, sc, "ws", dev), _buf(Wq_t, N * K, "Wq_t", dev), _buf(ws_t, sc, "ws_t", dev), raw)
 
 
 def fp8mlp_linear_fwd_block(M, K, N, xq, xs, Wq, ws, y, stream=None):
+    dev, raw = _here(stream)
     kb = _kblocks(K)
-    return _call("fp8mlp_linear_fwd_block", M, K, N, _buf(xq, M * K, "xq"), _buf(xs, 4 * M * kb, "xs"),
-                 _buf(Wq, N * K, "Wq"), _buf(ws, 4 * kb * _kblocks(N), "ws"), _buf(y, 2 * M * N, "y"),
-                 _stream(stream))
+    return _call("fp8mlp_linear_fwd_block", M, K, N, _buf(xq, M * K, "xq", dev), _buf(xs, 4 * M * kb, "xs", dev),
+                 _buf(Wq, N * K, "Wq", dev), _buf(ws, 4 * kb * _kblocks(N), "ws", dev), _buf(y, 2 * M * N, "y", dev),
+                 raw)
 
 
 def fp8mlp_linear_block(M, K, N, x, Wq, ws, xq, xs, y, stream=None):
+    dev, raw = _here(stream)
     kb = _kblocks(K)
-    return _call("fp8mlp_linear_block", M, K, N, _buf(x, 2 * M * K, "x"), _buf(Wq, N * K, "Wq"),
-                 _buf(ws, 4 * kb * _kblocks(N), "ws"), _buf(xq, M * K, "xq"), _buf(xs, 4 * M * kb, "xs"),
-                 _buf(y, 2 * M * N, "y"), _stream(stream))
+    return _call("fp8mlp_linear_block", M, K, N, _buf(x, 2 * M * K, "x", dev), _buf(Wq, N * K, "Wq", dev),
+                 _buf(ws, 4 * kb * _kblocks(N), "ws", dev), _buf(xq, M * K, "xq", dev), _buf(xs, 4 * M * kb, "xs", dev),
+                 _buf(y, 2 * M * N, "y", dev), raw)
 
 
 def fp8mlp_up_proj_block(M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, stream=None):
+    dev, raw = _here(stream)
     kd, kh = _kblocks(d), _kblocks(h)
-    return _call("fp8mlp_up_proj_block", M, d, h, _buf(xq, M * d, "xq"), _buf(xs, 4 * M * kd, "xs"),
-                 _buf(W1q, h * d, "W1q"), _buf(w1s, 4 * kd * kh, "w1s"), _buf(post, 2 * M * h, "post"),
-                 _buf(post_q, M * h, "post_q"), _buf(post_s, 4 * M * kh, "post_s"), _stream(stream))
+    return _call("fp8mlp_up_proj_block", M, d, h, _buf(xq, M * d, "xq", dev), _buf(xs, 4 * M * kd, "xs", dev),
+                 _buf(W1q, h * d, "W1q", dev), _buf(w1s, 4 * kd * kh, "w1s", dev), _buf(post, 2 * M * h, "post", dev),
+                 _buf(post_q, M * h, "post_q", dev), _buf(post_s, 4 * M * kh, "post_s", dev), raw)
 
 
 def fp8mlp_mlp_fwd_block(M, d, h, x, W1q, w1s, W2q_t, w2s_t, xq, xs, post, post_q, post_s, out, stream=None):
+    dev, raw = _here(stream)
     kd, kh = _kblocks(d), _kblocks(h)
-    return _call("fp8mlp_mlp_fwd_block", M, d, h, _buf(x, 2 * M * d, "x"), _buf(W1q, h * d, "W1q"),
-                 _buf(w1s, 4 * kd * kh, "w1s"), _buf(W2q_t, h * d, "W2q_t"), _buf(w2s_t, 4 * kd * kh, "w2s_t"),
-                 _buf(xq, M * d, "xq"), _buf(xs, 4 * M * kd, "xs"), _buf(post, 2 * M * h, "post"),
-                 _buf(post_q, M * h, "post_q"), _buf(post_s, 4 * M * kh, "post_s"), _buf(out, 2 * M * d, "out"),
-                 _stream(stream))
+    return _call("fp8mlp_mlp_fwd_block", M, d, h, _buf(x, 2 * M * d, "x", dev), _buf(W1q, h * d, "W1q", dev),
+                 _buf(w1s, 4 * kd * kh, "w1s", dev), _buf(W2q_t, h * d, "W2q_t", dev), _buf(w2s_t, 4 * kd * kh, "w2s_t", dev),
+                 _buf(xq, M * d, "xq", dev), _buf(xs, 4 * M * kd, "xs", dev), _buf(post, 2 * M * h, "post", dev),
+                 _buf(post_q, M * h, "post_q", dev), _buf(post_s, 4 * M * kh, "post_s", dev), _buf(out, 2 * M * d, "out", dev),
+                 raw)
 
 
 def _gate_rows(M, rows_per_gate):
@@ -428,12 +484,13 @@ def _gate_rows(M, rows_per_gate):
 
 def fp8mlp_norm_gate_fwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, w_pre, eps, r_next, rstd_post, x, rstd_pre,
                          xq=None, xs=None, stream=None):
+    dev, raw = _here(stream)
     n = 2 * M * d
-    return _call("fp8mlp_norm_gate_fwd", M, d, _buf(r, n, "r"), _buf(y, n, "y"), _buf(w_post, 2 * d, "w_post"),
-                 _buf(gate, 2 * d * _gate_rows(M, rows_per_gate), "gate"), rows_per_gate, _buf(alpha, 4, "alpha"),
-                 _buf(w_pre, 2 * d, "w_pre"), eps, _buf(r_next, n, "r_next"), _buf(rstd_post, 4 * M, "rstd_post"),
-                 _buf(x, n, "x"), _buf(rstd_pre, 4 * M, "rstd_pre"), _buf(xq, M * d, "xq"),
-                 _buf(xs, 4 * M * _kblocks(d), "xs"), _stream(stream))
+    return _call("fp8mlp_norm_gate_fwd", M, d, _buf(r, n, "r", dev), _buf(y, n, "y", dev), _buf(w_post, 2 * d, "w_post", dev),
+                 _buf(gate, 2 * d * _gate_rows(M, rows_per_gate), "gate", dev), rows_per_gate, _buf(alpha, 4, "alpha", dev),
+                 _buf(w_pre, 2 * d, "w_pre", dev), eps, _buf(r_next, n, "r_next", dev), _buf(rstd_post, 4 * M, "rstd_post", dev),
+                 _buf(x, n, "x", dev), _buf(rstd_pre, 4 * M, "rstd_pre", dev), _buf(xq, M * d, "xq", dev),
+                 _buf(xs, 4 * M * _kblocks(d), "xs", dev), raw)
 
 
 def fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate):
@@ -442,15 +499,16 @@ def fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate):
 
 def fp8mlp_norm_gate_bwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, rstd_post, r_next, w_pre, rstd_pre, dx,
                          dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, workspace, stream=None):
+    dev, raw = _here(stream)
     n, g = 2 * M * d, _gate_rows(M, rows_per_gate)
     need = int(lib.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate))
-    return _call("fp8mlp_norm_gate_bwd", M, d, _buf(r, n, "r"), _buf(y, n, "y"), _buf(w_post, 2 * d, "w_post"),
-                 _buf(gate, 2 * d * g, "gate"), rows_per_gate, _buf(alpha, 4, "alpha"),
-                 _buf(rstd_post, 4 * M, "rstd_post"), _buf(r_next, n, "r_next"), _buf(w_pre, 2 * d, "w_pre"),
-                 _buf(rstd_pre, 4 * M, "rstd_pre"), _buf(dx, n, "dx"), _buf(dr_next, n, "dr_next"), _buf(dr, n, "dr"),
-                 _buf(dy, n, "dy"), _buf(dw_post, 4 * d, "dw_post"), _buf(dgate, 4 * d * g, "dgate"),
-                 _buf(dalpha, 4, "dalpha"), _buf(dw_pre, 4 * d, "dw_pre"), _buf(workspace, need, "workspace"),
-                 _stream(stream))
+    return _call("fp8mlp_norm_gate_bwd", M, d, _buf(r, n, "r", dev), _buf(y, n, "y", dev), _buf(w_post, 2 * d, "w_post", dev),
+                 _buf(gate, 2 * d * g, "gate", dev), rows_per_gate, _buf(alpha, 4, "alpha", dev),
+                 _buf(rstd_post, 4 * M, "rstd_post", dev), _buf(r_next, n, "r_next", dev), _buf(w_pre, 2 * d, "w_pre", dev),
+                 _buf(rstd_pre, 4 * M, "rstd_pre", dev), _buf(dx, n, "dx", dev), _buf(dr_next, n, "dr_next", dev), _buf(dr, n, "dr", dev),
+                 _buf(dy, n, "dy", dev), _buf(dw_post, 4 * d, "dw_post", dev), _buf(dgate, 4 * d * g, "dgate", dev),
+                 _buf(dalpha, 4, "dalpha", dev), _buf(dw_pre, 4 * d, "dw_pre", dev), _buf(workspace, need, "workspace", dev),
+                 raw)
 
 
 class AdamwTensor(ctypes.Structure):
@@ -462,10 +520,11 @@ class AdamwTensor(ctypes.Structure):
 def adamw_tensor(n, p, p_bf16, g, m, v, m_scale=None, v_scale=None, lr_mult=1.0, weight_decay=0.0, state_bits=32):
     """One descriptor for :func:`fp8mlp_adamw_step`, its tensors' sizes checked.
     It holds addresses: the tensors have to stay alive."""
+    dev = _here(0)[0]
     sb, nb = state_bits // 8, 4 * _kblocks(n)
-    return AdamwTensor(n, _buf(p, 4 * n, "p"), _buf(p_bf16, 2 * n, "p_bf16"), _buf(g, 4 * n, "g"),
-                       _buf(m, sb * n, "m"), _buf(v, sb * n, "v"), _buf(m_scale, nb, "m_scale"),
-                       _buf(v_scale, nb, "v_scale"), lr_mult, weight_decay)
+    return AdamwTensor(n, _buf(p, 4 * n, "p", dev), _buf(p_bf16, 2 * n, "p_bf16", dev), _buf(g, 4 * n, "g", dev),
+                       _buf(m, sb * n, "m", dev), _buf(v, sb * n, "v", dev), _buf(m_scale, nb, "m_scale", dev),
+                       _buf(v_scale, nb, "v_scale", dev), lr_mult, weight_decay)
 
 
 def adamw_tensors(descriptors):
@@ -480,7 +539,8 @@ def _tensors(arr):
 
 
 def fp8mlp_adamw_state_init(st, lr, seed=0, step=0, stream=None):
-    return _call("fp8mlp_adamw_state_init", _buf(st, 32, "st"), lr, seed, step, _stream(stream))
+    dev, raw = _here(stream)
+    return _call("fp8mlp_adamw_state_init", _buf(st, 32, "st", dev), lr, seed, step, raw)
 
 
 def fp8mlp_grad_norm_workspace_size(tensors):
@@ -488,14 +548,16 @@ def fp8mlp_grad_norm_workspace_size(tensors):
 
 
 def fp8mlp_grad_norm(tensors, max_norm, norm_coef, workspace, stream=None):
+    dev, raw = _here(stream)
     need = int(lib.fp8mlp_grad_norm_workspace_size(*_tensors(tensors)))
-    return _call("fp8mlp_grad_norm", *_tensors(tensors), max_norm, _buf(norm_coef, 8, "norm_coef"),
-                 _buf(workspace, need, "workspace"), _stream(stream))
+    return _call("fp8mlp_grad_norm", *_tensors(tensors), max_norm, _buf(norm_coef, 8, "norm_coef", dev),
+                 _buf(workspace, need, "workspace", dev), raw)
 
 
 def fp8mlp_adamw_step(tensors, st, state_bits, beta1, beta2, eps, grad_coef=None, stream=None):
-    return _call("fp8mlp_adamw_step", *_tensors(tensors), _buf(st, 32, "st"), state_bits, beta1, beta2, eps,
-                 _buf(grad_coef, 4, "grad_coef"), _stream(stream))
+    dev, raw = _here(stream)
+    return _call("fp8mlp_adamw_step", *_tensors(tensors), _buf(st, 32, "st", dev), state_bits, beta1, beta2, eps,
+                 _buf(grad_coef, 4, "grad_coef", dev), raw)
 
 
 def fp8mlp_get_device_status(stream=None):

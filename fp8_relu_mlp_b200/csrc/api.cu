@@ -973,6 +973,11 @@ namespace {
 int block_product(bool relu2, int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
                   const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di,
                   cudaStream_t stream) {
+  if (!relu2 && block_gemv_fits(M, K, N)) {
+    const cudaError_t e = launch_block_gemv(M, K, N, nullptr, const_cast<uint8_t*>(xq), const_cast<float*>(xs), Wq, ws, out,
+                                            di->num_sms, stream);
+    return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "linear_fwd_block launch");
+  }
   BlockGemmParams p{};
   const bool pairs = block_gemm_pairs(M, N, di->num_sms);
   TRY(map_kmajor(&p.tmA, xq, U8, 1, M, K, kGemmBM, "xq"));
@@ -1082,6 +1087,10 @@ int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* W
   REQUIRE_PTR(y);
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
+  if (block_gemv_fits(M, K, N)) {
+    const cudaError_t e = launch_block_gemv(M, K, N, x, xq, xs, Wq, ws, y, di->num_sms, stream);
+    return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "linear_block launch");
+  }
   TRY(quantize_rows(M, K, x, xq, xs, stream));
   return block_product(false, M, K, N, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
 }

@@ -2,6 +2,8 @@
 // the optimizer step.
 #pragma once
 
+#include <atomic>
+
 #include "gemm_block_sm100.cuh"
 #include "internal.h"
 
@@ -9,10 +11,55 @@ namespace fp8mlp {
 
 constexpr int kBlock = 128;  // elements that share one scale
 
+namespace dev {
+
+// magnitude bits of the largest of eight BF16 values (NaN above infinity
+// above every finite value, so an integer max is exact)
+__device__ __forceinline__ unsigned int amax8(const uint4& v) {
+  const unsigned int w[4] = {v.x, v.y, v.z, v.w};
+  unsigned int m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+  return m;
+}
+
+__device__ __forceinline__ uint2 quant8(const uint4& v, float s) {
+  const unsigned int w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = pack_e4m3x2(__fmul_rn(bf16lo_to_f32(w[j]), s), __fmul_rn(bf16hi_to_f32(w[j]), s));
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+}  // namespace dev
+
+// Sets a kernel's shared memory limit once per device; two threads racing here
+// set the same value.
+template <class F>
+cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[64], int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 // whether a product of these sizes runs on 256 x 256 tiles of CTA pairs (else
 // on 128 x 128 tiles of single CTAs)
 bool block_gemm_pairs(int M, int N, int num_sms);
 cudaError_t launch_block_gemm(bool relu2, bool pairs, BlockGemmParams& p, int num_sms, cudaStream_t s);
+
+// the product for few rows; x: bf16, quantised on the way (xq and xs are
+// written), or NULL: xq and xs are read
+constexpr int kGemvMaxM = 8;
+bool block_gemv_fits(int M, int K, int N);
+cudaError_t launch_block_gemv(int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
+                              const float* ws, uint16_t* y, int num_sms, cudaStream_t s);
 
 cudaError_t launch_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, cudaStream_t s);
 cudaError_t launch_weight_block(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t, float* ws_t,

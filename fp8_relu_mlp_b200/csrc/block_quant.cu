@@ -7,24 +7,6 @@ namespace {
 
 using namespace dev;
 
-// magnitude bits of the largest of eight BF16 values (NaN above infinity
-// above every finite value, so an integer max is exact)
-__device__ __forceinline__ unsigned int amax8(const uint4& v) {
-  const unsigned int w[4] = {v.x, v.y, v.z, v.w};
-  unsigned int m = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-  return m;
-}
-
-__device__ __forceinline__ uint2 quant8(const uint4& v, float s) {
-  const unsigned int w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t q[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = pack_e4m3x2(__fmul_rn(bf16lo_to_f32(w[j]), s), __fmul_rn(bf16hi_to_f32(w[j]), s));
-  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-}
-
 // x [M,K] bf16 -> codes and inverse scales of groups of 128 along K.  Sixteen
 // lanes hold one group (16 bytes each), so its maximum takes four shuffles.
 // A half-warp walks kGroups groups of one row, all loads first: 64 bytes in

@@ -841,26 +841,10 @@ __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateB
   }
 }
 
-// sets a kernel's shared memory limit once per device; two threads racing here
-// set the same value
-template <class F>
-cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[64]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < 64;
-  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCta);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
-  return e;
-}
-
 template <int VPT, int LPR, bool CTA>
 cudaError_t fwd_one(const NormGateFwd& p, const NormShape& sh, bool ring_gate, cudaStream_t s) {
   static std::atomic<bool> done[64] = {};
-  cudaError_t e = allow_smem(norm_gate_fwd_kernel<VPT, LPR, CTA>, done);
+  cudaError_t e = allow_smem(norm_gate_fwd_kernel<VPT, LPR, CTA>, done, kSmemCta);
   if (e != cudaSuccess) return e;
   const int most = kSms * sh.per_sm;
   e = launch_pdl(norm_gate_fwd_kernel<VPT, LPR, CTA>, dim3(p.M < most ? p.M : most), dim3(sh.threads), sh.smem, s, p,
@@ -873,7 +857,7 @@ template <int VPT, int LPR, bool CTA>
 cudaError_t bwd_one(const NormGateBwd& p, const NormBwdSplit& sp, const NormShape& sh, bool ring_gate, bool direct,
                     cudaStream_t s) {
   static std::atomic<bool> done[64] = {};
-  cudaError_t e = allow_smem(norm_gate_bwd_kernel<VPT, LPR, CTA>, done);
+  cudaError_t e = allow_smem(norm_gate_bwd_kernel<VPT, LPR, CTA>, done, kSmemCta);
   if (e != cudaSuccess) return e;
   e = launch_pdl(norm_gate_bwd_kernel<VPT, LPR, CTA>, dim3(sp.ctas), dim3(sh.threads), sh.smem, s, p, sp,
                  fast_div(sp.rpg), sh.depth, ring_gate, direct);

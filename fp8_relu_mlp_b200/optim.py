@@ -32,6 +32,7 @@ class AdamW:
         self._plan = self._workspace = None
         self.state = torch.zeros(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
         self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
+        self._coef = self.norm[1:]
         A.fp8mlp_adamw_state_init(self.state, lr, seed & 0xFFFFFFFF, step_count, stream)
 
     def add(self, grad, master=None, weight=None, weight_decay: float = 0.0, lr_mult: float = 1.0, state=None) -> dict:
@@ -87,7 +88,7 @@ class AdamW:
         coef = None
         if self.max_norm is not None:
             A.fp8mlp_grad_norm(self._plan, self.max_norm, self.norm, self._workspace, self.stream)
-            coef = self.norm[1:]
+            coef = self._coef
         A.fp8mlp_adamw_step(self._plan, self.state, self.state_bits, *self.betas, self.eps, coef, self.stream)
 
     def read_state(self) -> dict:

@@ -102,7 +102,8 @@ def within(got, exact, mag, terms):
 
 
 # (M, K, N): one token up to several tiles of both tile sizes, ragged in each direction
-SHAPES = [(1, 16, 16), (1, 768, 2304), (2, 128, 128), (5, 144, 272), (8, 400, 48), (16, 2064, 400), (17, 768, 144),
+SHAPES = [(1, 16, 16), (1, 768, 2304), (2, 128, 128), (5, 144, 272), (8, 400, 48), (3, 1040, 2320), (4, 2064, 16), (6, 112, 144), (7, 4112, 48),
+          (1, 768, 50304), (2, 16400, 32), (8, 4112, 48), (8, 2064, 4112), (16, 2064, 400), (17, 768, 144),
           (64, 256, 768), (127, 112, 128), (129, 1040, 400), (256, 128, 256), (257, 384, 1296), (300, 768, 3088),
           (2049, 272, 768), (4096, 256, 2048), (4999, 400, 2320)]
 
