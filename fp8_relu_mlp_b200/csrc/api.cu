@@ -982,8 +982,8 @@ int block_product(bool relu2, int M, int K, int N, const uint8_t* xq, const floa
   const bool pairs = block_gemm_pairs(M, N, di->num_sms);
   TRY(map_kmajor(&p.tmA, xq, U8, 1, M, K, kGemmBM, "xq"));
   TRY(map_kmajor(&p.tmB, Wq, U8, 1, N, K, 128, "Wq"));
-  TRY(map2d(&p.tmOut, out, BF16, 2, N, M, 64, 32, SW128, "output"));
-  if (relu2) TRY(map2d(&p.tmOut2, post_q, U8, 1, N, M, 128, 32, SW128, "post_q"));
+  TRY(map2d(&p.tmOut, out, BF16, 2, N, M, 64, pairs ? 128 : 32, SW128, "output"));
+  if (relu2) TRY(map2d(&p.tmOut2, post_q, U8, 1, N, M, 128, pairs ? 128 : 32, SW128, "post_q"));
   p.M = M;
   p.N = N;
   p.K = K;

@@ -8,11 +8,11 @@ namespace fp8mlp {
 namespace {
 
 // large problems: 256 x 256 tiles of a CTA pair
-using CfgLin2 = BlockCfg<2, 256, 128, 5, false, 2>;
-using CfgUp2 = BlockCfg<2, 256, 128, 5, true, 1>;
+using CfgLin2 = BlockCfg<2, 256, 5, false>;
+using CfgUp2 = BlockCfg<2, 256, 4, true>;
 // few tiles: 128 x 128 tiles of one CTA, so that more SMs take part
-using CfgLin1 = BlockCfg<1, 128, 128, 6, false, 2>;
-using CfgUp1 = BlockCfg<1, 128, 128, 6, true, 1>;
+using CfgLin1 = BlockCfg<1, 128, 6, false>;
+using CfgUp1 = BlockCfg<1, 128, 5, true>;
 
 constexpr int kMaxDevices = 64;
 

@@ -13,7 +13,8 @@
 // thread holds a whole 1 x 128 scale block, so its maximum needs no exchange.
 //   warp 0      TMA producer: A/B k-blocks into a STAGES-deep ring
 //   warp 1      allocates TMEM, issues the UMMAs from one thread
-//   then        4 * BN / 128 epilogue warps (from warp 2, or 4 with 8 of them)
+//   warp 2      pairs: stores finished tiles (TMA)
+//   then        4 * BN / 128 epilogue warps
 // CG = 2: the CTAs of a cluster pair share a 2-CTA UMMA over 256 rows, as in
 // gemm_sm100.cuh.  TMA zero-fills rows and columns past the edges and clips
 // the stores.
@@ -25,8 +26,8 @@ namespace fp8mlp {
 
 struct alignas(64) BlockGemmParams {
   CUtensorMap tmA, tmB;
-  CUtensorMap tmOut;   // bf16 output, 32 rows x 64 columns
-  CUtensorMap tmOut2;  // relu^2: e4m3 copy, 32 rows x WC columns
+  CUtensorMap tmOut;   // bf16 output, STORE_ROWS rows x 64 columns
+  CUtensorMap tmOut2;  // relu^2: e4m3 copy, STORE_ROWS rows x 128 columns
   int M, N, K;
   int tiles_m, tiles_n;
   int n_blocks;          // ceil(N / 128): row length of ws
@@ -38,15 +39,13 @@ struct alignas(64) BlockGemmParams {
   int debug_flags;
 };
 
-// CG CTAs per tile, BN tile columns, WC columns per epilogue warp, NOUT output
-// slots of 64 columns per warp
-template <int CG_, int BN_, int WC_, int STAGES_, bool RELU2_, int NOUT_>
+// CG CTAs per tile, BN tile columns
+template <int CG_, int BN_, int STAGES_, bool RELU2_>
 struct BlockCfg {
   static constexpr int CG = CG_;
   static constexpr int BM = 128;
   static constexpr int TILE_M = BM * CG;
   static constexpr int BN = BN_;
-  static constexpr int WC = WC_;
   static constexpr int B_ROWS = BN / CG;           // rows of B per CTA
   static constexpr int STAGES = STAGES_;
   static constexpr bool RELU2 = RELU2_;
@@ -57,25 +56,28 @@ struct BlockCfg {
   static constexpr int STAGE_TX = CG * STAGE_BYTES;
   static constexpr uint32_t IDESC = dev::instr_desc(dev::FMT_E4M3, dev::FMT_E4M3, false, false, TILE_M, BN);
   static constexpr int NBUF = 512 / BN;            // TMEM accumulators
-  static constexpr int NEPI = 4 * BN / WC;
-  // From eight epilogue warps on a thread needs more than its even share of
-  // the registers: the first warpgroup (producer, issuer, two idle warps)
-  // hands some over.
-  static constexpr bool SPLIT_REGS = NEPI >= 8;
-  static constexpr int EPI0 = SPLIT_REGS ? 4 : 2;  // first epilogue warp
+  static constexpr int NEPI = 4 * BN / 128;
+  // A pair's CTAs have tile after tile: a thread of its own stores them, since
+  // a TMA store waits for its place in the queue, up to 1000 cycles behind the
+  // others of its tile and the loads, which the epilogue would lose.  A single
+  // CTA has one tile, mostly: each epilogue warp stores its part when it has
+  // it, which ends 0.4 us sooner than gathering the warps' parts.
+  static constexpr bool STORE_WARP = CG == 2;
+  static constexpr int STORE_ROWS = STORE_WARP ? 128 : 32;
+  static constexpr int EPI0 = STORE_WARP ? 4 : 2;  // first epilogue warp
   static constexpr int THREADS = 32 * (EPI0 + NEPI);
+  // With eight epilogue warps a thread needs more than its even share of the
+  // registers: the first warpgroup hands some over.
+  static constexpr bool SPLIT_REGS = NEPI == 8;
   static constexpr int REGS_CONTROL = 40, REGS_EPI = 232;
   static constexpr int REGS_SUM = 128 * REGS_CONTROL + 32 * NEPI * REGS_EPI;  // of the launch, at least
-  // output slots of a warp: 64 columns of bf16 each, and the e4m3 copy
-  static constexpr int OUT_BUF = 32 * 128;
-  static constexpr int NOUT = NOUT_;
-  static constexpr int SLOT = NOUT * OUT_BUF + (RELU2 ? 32 * WC : 0);
-  static constexpr int XCHG_BYTES = RELU2 && WC == 64 ? NEPI * 32 * 4 : 0;
-  static constexpr int NUM_BARS = 2 * STAGES + NBUF + 1;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NEPI * SLOT + XCHG_BYTES + NUM_BARS * 8 + 16;
+  // output: chunks of 128 rows x 128 bytes, 64 columns of bf16 or 128 codes
+  static constexpr int CHUNK = BM * 128;
+  static constexpr int OUT_CHUNKS = BN / 64 + (RELU2 ? BN / 128 : 0);
+  static constexpr int NUM_BARS = 2 * STAGES + NBUF + 3;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + OUT_CHUNKS * CHUNK + NUM_BARS * 8 + 16;
   static_assert(CG == 1 || CG == 2, "CTA group");
   static_assert(BN == 128 || BN == 256, "accumulators");
-  static_assert(WC == 128 || WC == 64, "columns per epilogue warp");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -88,10 +90,6 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // A load that stays where it is written: the compiler would sink a plain one
@@ -143,12 +141,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sStage = smem;
-  uint8_t* sEpi = sStage + C::STAGES * C::STAGE_BYTES;
-  float* sXchg = reinterpret_cast<float*>(sEpi + C::NEPI * C::SLOT);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::NEPI * C::SLOT + C::XCHG_BYTES);
+  uint8_t* sOut = sStage + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_CHUNKS * C::CHUNK);
   uint64_t* done = full + C::STAGES;
   uint64_t* tempty = done + C::STAGES;
-  uint64_t* fin = tempty + C::NBUF;
+  uint64_t* oready = tempty + C::NBUF;  // a tile's output is in shared memory
+  uint64_t* ofree = oready + 1;         // it has been read from there
+  uint64_t* fin = ofree + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -167,6 +166,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     for (int a = 0; a < C::NBUF; ++a) {
       mbar_init(&tempty[a], C::NEPI * CG);  // one arrival per epilogue warp of the pair
     }
+    mbar_init(oready, C::NEPI);
+    mbar_init(ofree, 1);
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -272,18 +273,41 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
           tc_commit_cg2(fin);
         mbar_wait_drain(fin, 0, p.timeout_ns);
       }
+    } else if (C::STORE_WARP && warp == 2) {
+      // ---------------------------------------------------------- store
+      if (lane == 0) {
+        uint32_t phase = 0;
+        for (int t = unit; t < num_tiles; t += nunits) {
+          const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
+          const int row0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM;
+          if (!mbar_wait(oready, phase, w)) break;
+#pragma unroll
+          for (int c = 0; c < C::BN / 64; ++c) tma_store_2d(&p.tmOut, sOut + c * C::CHUNK, nb * C::BN + c * 64, row0);
+          if constexpr (C::RELU2) {
+#pragma unroll
+            for (int c = 0; c < C::BN / 128; ++c)
+              tma_store_2d(&p.tmOut2, sOut + (C::BN / 64 + c) * C::CHUNK, nb * C::BN + c * 128, row0);
+          }
+          bulk_commit();
+          bulk_wait_read<0>();
+          mbar_arrive(ofree);
+          phase ^= 1u;
+        }
+        bulk_wait<0>();
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (C::SPLIT_REGS) reg_inc<C::REGS_EPI>();
     const int q = warp & 3;  // TMEM lane quarter
     const int e = warp - C::EPI0;
-    const int c0 = (e >> 2) * C::WC;  // first column of the tile that is this warp's
+    const int c0 = (e >> 2) * 128;  // first column of the tile that is this warp's
     const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0;
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
-    uint8_t* slot = sEpi + e * C::SLOT;
-    const uint32_t sbase = smem_u32(slot);
-    uint32_t buf = 0, stage = 0, phase = 0;
+    const uint32_t orow = smem_u32(sOut) + (e >> 2) * (2 * C::CHUNK) + (q * 32 + lane) * 128;  // this thread's row, bf16
+    const uint32_t qrow = smem_u32(sOut) + (C::BN / 64 + (e >> 2)) * C::CHUNK + (q * 32 + lane) * 128;  // codes
+    const uint32_t xor16 = (lane & 7) << 4;  // of the 128-byte swizzle
+    uint32_t buf = 0, stage = 0, phase = 0, ofree_phase = 1;
 
     // This thread's two scales, read two k-blocks ahead and across tiles: the
     // next tile's first ones are under way while the current one is written.
@@ -312,14 +336,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     scales(a0, b0);
     scales(a1, b1);
 
+    // this warp's rows of a chunk, out
+    auto store_part = [&](const CUtensorMap* map, int chunk, int col, int row) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(map, sOut + chunk * C::CHUNK + q * 4096, col, row);
+        bulk_commit();
+      }
+    };
     bool ok = true;
     for (int t = unit; t < num_tiles; t += nunits) {
       const int mb = t / p.tiles_n, nb = t - mb * p.tiles_n;
       const int row0 = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32;
       const int n0 = nb * C::BN + c0;
-      uint64_t acc[C::WC / 2];  // fp32 sums as pairs
+      uint64_t acc[64];  // 128 fp32 sums as pairs
 #pragma unroll
-      for (int i = 0; i < C::WC / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
         const float f = __fmul_rn(a0, b0);
         const uint64_t f2 = f2_pack(f, f);
@@ -336,9 +369,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         const uint32_t src = tmem_mine + buf * C::BN;
         tmem_ld16_issue(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < C::WC / 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           tmem_wait16(v[c & 1]);
-          if (c < C::WC / 16 - 1) {
+          if (c < 7) {
             tmem_ld16_issue(src + (c + 1) * 16, v[(c + 1) & 1]);
           } else {
             tc_fence_before();
@@ -369,7 +402,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         // rounded once, from the fp32 value.
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::WC / 2; ++i) {
+        for (int i = 0; i < 64; ++i) {
           float u, v;
           f2_unpack(acc[i], u, v);
           amax = max3_nan(amax, u, v);
@@ -379,48 +412,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
           acc[i] = f2_mul(t, t);
         }
         amax = __fmul_rn(amax, amax);  // squaring is monotone, its rounding too
-        if constexpr (C::WC == 64) {
-          // the two warps that share the block exchange their maxima
-          const int pair = ((e >> 3) << 2) + q;
-          sXchg[e * 32 + lane] = amax;
-          named_barrier(1 + pair, 64);
-          amax = max_nan(amax, sXchg[(e ^ 4) * 32 + lane]);
-          named_barrier(1 + pair, 64);
-        }
         float inv;
         s = block_scale(amax, &inv);
-        if ((c0 & 127) == 0 && row0 + lane < p.M && n0 < p.N)
+        if (row0 + lane < p.M && n0 < p.N)
           p.post_s[static_cast<size_t>(n0 >> 7) * p.M + row0 + lane] = inv;
       }
-      if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have left their slots
-      __syncwarp();
-      // 64 columns of bf16 to a slot and out
-      auto put = [&](int c) {
-        const int off = C::NOUT == 2 ? c * C::OUT_BUF : 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float u, v;
-            f2_unpack(acc[c * 32 + j * 4 + i], u, v);
-            pk[i] = pack_bf16x2(u, v);
-          }
-          st_shared_v4(sbase + off + swz<7>(lane * 128 + j * 16), pk[0], pk[1], pk[2], pk[3]);
-        }
-        fence_proxy_async_smem();
+      // the previous tile has left shared memory
+      if constexpr (C::STORE_WARP) {
+        if (!mbar_wait_inline(ofree, ofree_phase, w)) break;
+        ofree_phase ^= 1u;
+      } else {
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&p.tmOut, slot + off, n0 + c * 64, row0);
-          bulk_commit();
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u, v;
+          f2_unpack(acc[j * 4 + i], u, v);
+          pk[i] = pack_bf16x2(u, v);
         }
-      };
-      put(0);
+        st_shared_v4(orow + (j >> 3) * C::CHUNK + (((j & 7) * 16) ^ xor16), pk[0], pk[1], pk[2], pk[3]);
+        if (!C::STORE_WARP && (j & 7) == 7) store_part(&p.tmOut, j >> 3, n0 + (j >> 3) * 64, row0);
+      }
       if constexpr (C::RELU2) {
-        const uint32_t qb = sbase + C::NOUT * C::OUT_BUF;
         const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-        for (int j = 0; j < C::WC / 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           uint32_t qk[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -429,24 +449,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
             f2_unpack(f2_mul(acc[j * 8 + 2 * i + 1], s2), u2, u3);
             qk[i] = pack_e4m3x2(u0, u1) | (pack_e4m3x2(u2, u3) << 16);
           }
-          st_shared_v4(qb + swz<C::WC / 16 - 1>(lane * C::WC + j * 16), qk[0], qk[1], qk[2], qk[3]);
+          st_shared_v4(qrow + ((j * 16) ^ xor16), qk[0], qk[1], qk[2], qk[3]);
         }
+        if (!C::STORE_WARP) store_part(&p.tmOut2, C::BN / 64, n0, row0);
+      }
+      if constexpr (C::STORE_WARP) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&p.tmOut2, slot + C::NOUT * C::OUT_BUF, n0, row0);
-          bulk_commit();
-        }
-      }
-      if constexpr (C::WC == 128) {
-        if constexpr (C::NOUT == 1) {
-          if (lane == 0) bulk_wait_read<1>();  // the first half has left the slot, the codes may be under way
-          __syncwarp();
-        }
-        put(1);
+        if (lane == 0) mbar_arrive(oready);
       }
     }
-    if (lane == 0) bulk_wait<0>();
+    if (!C::STORE_WARP && lane == 0) bulk_wait<0>();
     __syncwarp();
   }
 
