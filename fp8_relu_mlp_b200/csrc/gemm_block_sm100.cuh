@@ -117,6 +117,18 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
+// conversions of the positive part, NaN kept
+__device__ __forceinline__ uint32_t pack_bf16x2_relu(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.relu.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x2_relu(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return static_cast<uint32_t>(d);
+}
+
 // Scale of a block of 128 whose largest magnitude is `amax`: s maps amax onto
 // 448 and is at most 2^120, so that 1/s stays a normal number; an all-zero
 // block takes s = 1.  A block that holds an infinity or NaN takes s = 1 and
@@ -397,19 +409,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
       if (!ok) break;
       float s = 1.f;
       if constexpr (C::RELU2) {
-        // post = relu(acc)^2 in place, its maximum over this 1 x 128 block
-        // (columns past N are zero), and the block's scale.  The codes are
-        // rounded once, from the fp32 value.
+        // acc |acc| in place, whose positive part is post (the conversions drop
+        // the rest), the maximum over this 1 x 128 block (columns past N are
+        // zero), and the block's scale.  The codes are rounded once, from the
+        // fp32 value.
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           float u, v;
           f2_unpack(acc[i], u, v);
           amax = max3_nan(amax, u, v);
-          u = max_nan(u, 0.f);
-          v = max_nan(v, 0.f);
-          const uint64_t t = f2_pack(u, v);
-          acc[i] = f2_mul(t, t);
+          acc[i] = f2_pack(__fmul_rn(u, fabsf(u)), __fmul_rn(v, fabsf(v)));
         }
         amax = __fmul_rn(amax, amax);  // squaring is monotone, its rounding too
         float inv;
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         for (int i = 0; i < 4; ++i) {
           float u, v;
           f2_unpack(acc[j * 4 + i], u, v);
-          pk[i] = pack_bf16x2(u, v);
+          pk[i] = C::RELU2 ? pack_bf16x2_relu(u, v) : pack_bf16x2(u, v);
         }
         st_shared_v4(orow + (j >> 3) * C::CHUNK + (((j & 7) * 16) ^ xor16), pk[0], pk[1], pk[2], pk[3]);
         if (!C::STORE_WARP && (j & 7) == 7) store_part(&p.tmOut, j >> 3, n0 + (j >> 3) * 64, row0);
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
             float u0, u1, u2, u3;
             f2_unpack(f2_mul(acc[j * 8 + 2 * i], s2), u0, u1);
             f2_unpack(f2_mul(acc[j * 8 + 2 * i + 1], s2), u2, u3);
-            qk[i] = pack_e4m3x2(u0, u1) | (pack_e4m3x2(u2, u3) << 16);
+            qk[i] = pack_e4m3x2_relu(u0, u1) | (pack_e4m3x2_relu(u2, u3) << 16);
           }
           st_shared_v4(qrow + ((j * 16) ^ xor16), qk[0], qk[1], qk[2], qk[3]);
         }
