@@ -300,3 +300,114 @@ class MLPStack:
             A.fp8mlp_amax_reduce_update_scale(b.partial_amax, b.partial_amax.numel(), b.state, self.stream)
             if self.fp8_up:
                 self._update_x_scale(l)
+
+
+class BlockScaledStack:
+    """L residual layers with a scale for each block of 128 in place of the
+    delayed per-tensor scales (no calibration step, no amax to reduce):
+
+        x_l     = RMSNorm(r_l) w_pre_l
+        out_l   = MLP_l(x_l)
+        r_{l+1} = alpha_l r_l + gate_l (RMSNorm(out_l) w_post_l)
+
+    The end of one layer and the norm of the next are one launch, which also
+    writes x's FP8 copy.  ``rows_per_gate``: how many neighbouring rows share
+    a gate vector (None: all of them).  The backward is BF16 (:class:`MLPStack`'s);
+    with ``max_norm`` the optimizer clips.
+
+    Weights: ``W1``, ``W2`` (BF16 [h, d] per layer), ``w_pre``, ``w_post``
+    (BF16 [d]), ``gate`` (BF16), ``alpha`` (one fp32), one per layer.  Fill
+    them, then ``refresh_caches()``, then ``optimizer()``, which takes its
+    fp32 masters from them.  ``train_step`` (forward, backward, AdamW, caches)
+    launches only library calls, so it can be captured into a CUDA graph."""
+
+    def __init__(self, L: int, M: int, d: int, h: int, rows_per_gate: int | None = None, eps: float = 1e-6,
+                 device="cuda", stream=None):
+        self.L, self.M, self.d, self.h = L, M, d, h
+        self.rows = max(1, M if rows_per_gate is None else rows_per_gate)
+        self.eps, self.device, self.stream = eps, torch.device(device), stream
+        bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+
+        def each(*shape, dtype=bf, n=L, fill=None):
+            make = torch.empty if fill is None else (lambda *s, **k: torch.full(s, fill, **k))
+            return [make(*shape, dtype=dtype, device=self.device) for _ in range(n)]
+
+        kd, kh, G = -(-d // 128), -(-h // 128), -(-M // self.rows)
+        self.W1, self.W2 = each(h, d, fill=0.0), each(h, d, fill=0.0)
+        self.w_pre, self.w_post = each(d, fill=1.0), each(d, fill=1.0)
+        self.gate, self.alpha = each(G, d, fill=1.0), each(1, dtype=f32, fill=1.0)
+        self.W1q, self.w1s = each(h, d, dtype=u8), each(kd, kh, dtype=f32)
+        self.W2q_t, self.w2s_t = each(d, h, dtype=u8), each(kh, kd, dtype=f32)
+        # kept for the backward
+        self.r, self.x, self.out = each(M, d, n=L + 1), each(M, d), each(M, d)
+        self.post = each(M, h)
+        self.rstd_pre, self.rstd_post = each(M, dtype=f32), each(M, dtype=f32)
+        # of one layer at a time
+        self.xq, self.xs = each(M, d, dtype=u8, n=1)[0], each(kd, M, dtype=f32, n=1)[0]
+        self.post_q, self.post_s = each(M, h, dtype=u8, n=1)[0], each(kh, M, dtype=f32, n=1)[0]
+        self.dr, self.dOut, self.dX = (each(M, d, n=1, fill=0.0)[0] for _ in range(3))
+        self.dPre = each(M, h, n=1)[0]
+        self.dW1, self.dW2 = each(h, d, dtype=f32), each(h, d, dtype=f32)
+        self.dw_pre, self.dw_post = each(d, dtype=f32), each(d, dtype=f32)
+        self.dgate, self.dalpha = each(G, d, dtype=f32, fill=0.0), each(1, dtype=f32)
+        self.workspace = torch.empty(max(16, A.fp8mlp_norm_gate_bwd_workspace_size(M, d, self.rows)), dtype=u8,
+                                     device=self.device)
+
+    def refresh_caches(self):
+        """FP8 weight caches from the current weights."""
+        for l in range(self.L):
+            A.fp8mlp_weight_block_cache_refresh(self.h, self.d, self.W1[l], self.W1q[l], self.w1s[l], stream=self.stream)
+            A.fp8mlp_weight_block_cache_refresh(self.h, self.d, self.W2[l], None, None, self.W2q_t[l], self.w2s_t[l],
+                                                self.stream)
+
+    def forward(self):
+        """``r[0]`` -> ``r[L]``."""
+        M, d, h = self.M, self.d, self.h
+        A.fp8mlp_norm_gate_fwd(M, d, self.r[0], None, None, None, 1, None, self.w_pre[0], self.eps, None, None, self.x[0],
+                               self.rstd_pre[0], self.xq, self.xs, self.stream)
+        for l in range(self.L):
+            A.fp8mlp_up_proj_block(M, d, h, self.xq, self.xs, self.W1q[l], self.w1s[l], self.post[l], self.post_q,
+                                   self.post_s, self.stream)
+            A.fp8mlp_linear_fwd_block(M, h, d, self.post_q, self.post_s, self.W2q_t[l], self.w2s_t[l], self.out[l],
+                                      self.stream)
+            nxt = ((self.w_pre[l + 1], self.x[l + 1], self.rstd_pre[l + 1], self.xq, self.xs) if l + 1 < self.L else
+                   (None,) * 5)
+            A.fp8mlp_norm_gate_fwd(M, d, self.r[l], self.out[l], self.w_post[l], self.gate[l], self.rows, self.alpha[l],
+                                   nxt[0], self.eps, self.r[l + 1], self.rstd_post[l], *nxt[1:], self.stream)
+
+    def backward(self):
+        """``dr`` holds dL/dr_L on entry and dL/dr_0 on exit."""
+        M, d, h = self.M, self.d, self.h
+        for l in range(self.L - 1, -1, -1):
+            # the norm of layer l + 1 (none behind the last) and the gate of layer l
+            pre = ((self.w_pre[l + 1], self.rstd_pre[l + 1], self.dX) if l + 1 < self.L else (None,) * 3)
+            A.fp8mlp_norm_gate_bwd(M, d, self.r[l], self.out[l], self.w_post[l], self.gate[l], self.rows, self.alpha[l],
+                                   self.rstd_post[l], self.r[l + 1] if l + 1 < self.L else None, *pre, self.dr, self.dr,
+                                   self.dOut, self.dw_post[l], self.dgate[l], self.dalpha[l],
+                                   self.dw_pre[l + 1] if l + 1 < self.L else None, self.workspace, self.stream)
+            A.fp8mlp_mlp_bwd(M, d, h, self.x[l], self.W1[l], self.W2[l], self.post[l], self.dOut, self.dPre, self.dX,
+                             self.dW1[l], self.dW2[l], self.stream)
+        A.fp8mlp_norm_gate_bwd(M, d, None, None, None, None, 1, None, None, self.r[0], self.w_pre[0], self.rstd_pre[0],
+                               self.dX, self.dr, self.dr, None, None, None, None, self.dw_pre[0], self.workspace,
+                               self.stream)
+
+    def optimizer(self, state_bits: int = 8, masters: bool = True, weight_decay: float = 0.0, **kw):
+        """:class:`.optim.AdamW` over every weight; decay on W1 and W2 only.
+        ``masters=False`` keeps W1 and W2 in BF16 alone, rounded
+        stochastically.  ``kw`` goes to AdamW (lr, betas, max_norm, ...)."""
+        from .optim import AdamW
+        opt = AdamW(state_bits=state_bits, device=self.device, stream=self.stream, **kw)
+        for l in range(self.L):
+            for w, g in ((self.W1[l], self.dW1[l]), (self.W2[l], self.dW2[l])):
+                opt.add(g, master=w.float() if masters else None, weight=w, weight_decay=weight_decay)
+            for w, g in ((self.w_pre[l], self.dw_pre[l]), (self.w_post[l], self.dw_post[l]), (self.gate[l], self.dgate[l])):
+                opt.add(g, master=w.float(), weight=w)
+            opt.add(self.dalpha[l], master=self.alpha[l])
+        return opt
+
+    def train_step(self, opt):
+        """One step from ``r[0]`` and dL/dr_L in ``dr``."""
+        self.forward()
+        self.backward()
+        opt.step()
+        self.refresh_caches()

@@ -65,7 +65,12 @@ SHAPES = [(1, 16, 1), (1, 768, 1), (5, 32, 2), (33, 256, 33), (7, 272, 3), (100,
           (64, 784, 100), (65, 1024, 64), (17, 1040, 5), (40, 2048, 40), (9, 2064, 4), (6, 4096, 1), (5, 4112, 2), (3, 8192, 3)]
 
 
-@pytest.mark.parametrize("M,d,rows", SHAPES)
+# more rows than workers, so that each walks several, at every way of dealing rows out
+LONG = [(20000, 48, 20000), (40001, 32, 1), (20000, 64, 7), (9000, 128, 500), (6001, 256, 6001), (4000, 512, 1), (6000, 768, 100),
+        (3001, 1024, 9), (3000, 1040, 3000), (2000, 2064, 50), (1500, 4112, 1500), (700, 8192, 3)]
+
+
+@pytest.mark.parametrize("M,d,rows", SHAPES + LONG)
 def test_forward(M, d, rows):
     p = inputs(M, d, rows, seed=M + d)
     got = fwd(p, M, d, rows, quant=True)
@@ -187,7 +192,10 @@ def check(got, p, s, M, rows, post=True, pre=True, drn=True):
 
 
 @pytest.mark.parametrize("M,d,rows", SHAPES + [(2500, 768, 2500), (3000, 256, 700), (1300, 768, 1), (2000, 1040, 2000),
-                                               (1500, 16, 10), (1201, 512, 1200)])
+                                               (1500, 16, 10), (1201, 512, 1200)] + LONG + [
+    # gate rows dealt whole; shared by few and many workers; more of them than one CTA column each; runs that touch several
+    (30001, 768, 20), (3000, 768, 40), (16001, 256, 33), (5000, 1024, 101), (2500, 2064, 33), (9000, 64, 2999),
+    (1200, 768, 1199), (16, 768, 4), (17, 768, 4), (13, 400, 13)])
 def test_gradient_against_the_formula(M, d, rows):
     p = inputs(M, d, rows, seed=M + d)
     s = saved(p, M, d, rows)
