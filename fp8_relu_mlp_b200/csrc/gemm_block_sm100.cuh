@@ -104,6 +104,13 @@ __device__ __forceinline__ float ld_scale(const float* p, bool valid) {
   return v;
 }
 
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // max that keeps NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -248,26 +255,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0 && leader) {
+      // The whole warp runs the loop and one elected lane issues: what it
+      // issues is then known to be uniform and needs no moves to uniform
+      // registers, which took longer than the UMMAs.
+      if (leader) {
+        const bool elected = elect_one();
         uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
         bool ok = true;
         for (int t = unit; t < num_tiles && ok; t += nunits) {
           for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait(&full[stage], phase, w) || !mbar_wait(&tempty[buf], buf_phase ^ 1u, w)) {
+            if (!mbar_wait_inline(&full[stage], phase, w) || !mbar_wait_inline(&tempty[buf], buf_phase ^ 1u, w)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t a0 = smem_u32(sStage + stage * C::STAGE_BYTES);
             const uint32_t b0 = a0 + C::A_BYTES;
+            if (elected) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024),
-                             smem_desc(b0 + k * 32, 16, 1024), C::IDESC, k != 0 ? 1u : 0u);
-            if constexpr (CG == 1)
-              tc_commit(&done[stage]);
-            else
-              tc_commit_cg2_mc(&done[stage], 0x3);
+              for (int k = 0; k < 4; ++k)
+                umma<CG, true>(tmem_base + buf * C::BN, smem_desc(a0 + k * 32, 16, 1024),
+                               smem_desc(b0 + k * 32, 16, 1024), C::IDESC, k != 0 ? 1u : 0u);
+              if constexpr (CG == 1)
+                tc_commit(&done[stage]);
+              else
+                tc_commit_cg2_mc(&done[stage], 0x3);
+            }
+            __syncwarp();
             if (++buf == C::NBUF) {
               buf = 0;
               buf_phase ^= 1u;
@@ -278,12 +292,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
             }
           }
         }
-        // every UMMA this thread issued must be complete before TMEM is freed
-        if constexpr (CG == 1)
-          tc_commit(fin);
-        else
-          tc_commit_cg2(fin);
-        mbar_wait_drain(fin, 0, p.timeout_ns);
+        // every UMMA issued must be complete before TMEM is freed
+        if (elected) {
+          if constexpr (CG == 1)
+            tc_commit(fin);
+          else
+            tc_commit_cg2(fin);
+          mbar_wait_drain(fin, 0, p.timeout_ns);
+        }
+        __syncwarp();
       }
     } else if (C::STORE_WARP && warp == 2) {
       // ---------------------------------------------------------- store
