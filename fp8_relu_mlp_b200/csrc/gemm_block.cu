@@ -11,7 +11,7 @@ namespace {
 using CfgLin2 = BlockCfg<2, 256, 5, false>;
 using CfgUp2 = BlockCfg<2, 256, 4, true>;
 // few tiles: 128 x 128 tiles of one CTA, so that more SMs take part
-using CfgLin1 = BlockCfg<1, 128, 6, false>;
+using CfgLin1 = BlockCfg<1, 128, 5, false>;
 using CfgUp1 = BlockCfg<1, 128, 5, true>;
 
 constexpr int kMaxDevices = 64;

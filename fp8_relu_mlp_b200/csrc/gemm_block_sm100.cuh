@@ -14,6 +14,7 @@
 //   warp 0      TMA producer: A/B k-blocks into a STAGES-deep ring
 //   warp 1      allocates TMEM, issues the UMMAs from one thread
 //   warp 2      pairs: stores finished tiles (TMA)
+//   next        scales of each stage to shared memory
 //   then        4 * BN / 128 epilogue warps
 // CG = 2: the CTAs of a cluster pair share a 2-CTA UMMA over 256 rows, as in
 // gemm_sm100.cuh.  TMA zero-fills rows and columns past the edges and clips
@@ -64,18 +65,26 @@ struct BlockCfg {
   // it, which ends 0.4 us sooner than gathering the warps' parts.
   static constexpr bool STORE_WARP = CG == 2;
   static constexpr int STORE_ROWS = STORE_WARP ? 128 : 32;
-  static constexpr int EPI0 = STORE_WARP ? 4 : 2;  // first epilogue warp
+  static constexpr int SCALE_WARP = STORE_WARP ? 3 : 2;
+  static constexpr int EPI0 = SCALE_WARP + 1;      // first epilogue warp
   static constexpr int THREADS = 32 * (EPI0 + NEPI);
   // With eight epilogue warps a thread needs more than its even share of the
   // registers: the first warpgroup hands some over.
   static constexpr bool SPLIT_REGS = NEPI == 8;
-  static constexpr int REGS_CONTROL = 40, REGS_EPI = 232;
+  static constexpr int REGS_CONTROL = 72, REGS_EPI = 216;
   static constexpr int REGS_SUM = 128 * REGS_CONTROL + 32 * NEPI * REGS_EPI;  // of the launch, at least
   // output: chunks of 128 rows x 128 bytes, 64 columns of bf16 or 128 codes
   static constexpr int CHUNK = BM * 128;
   static constexpr int OUT_CHUNKS = BN / 64 + (RELU2 ? BN / 128 : 0);
+  // ring of scales: a k-block's are 128 rows' and BN / 128 weight blocks'.  A
+  // slot is free once the UMMAs NBUF k-blocks behind its last use are done
+  // (they waited for that use's accumulator); the wait for those must not see
+  // the barrier's next phase, which holds for SRING <= NBUF + STAGES.
+  static constexpr int SCALES = 132 * 4;
+  static constexpr int SRING = NBUF == 2 ? 4 : 8;
+  static_assert(SRING > NBUF && SRING <= NBUF + STAGES && SRING - NBUF <= STAGES, "scale ring");
   static constexpr int NUM_BARS = 2 * STAGES + NBUF + 3;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + OUT_CHUNKS * CHUNK + NUM_BARS * 8 + 16;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SRING * SCALES + OUT_CHUNKS * CHUNK + NUM_BARS * 8 + 16;
   static_assert(CG == 1 || CG == 2, "CTA group");
   static_assert(BN == 128 || BN == 256, "accumulators");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -102,6 +111,12 @@ __device__ __forceinline__ float ld_scale(const float* p, bool valid) {
       : "=f"(v)
       : "l"(p), "r"(static_cast<int>(valid)));
   return v;
+}
+
+// arrive on an mbarrier of another CTA of the pair, after this warp's stores to
+// its own shared memory (read by its own CTA only)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // one lane of a converged warp
@@ -157,11 +172,16 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_constant__ BlockGemmParams p) {
   using namespace dev;
   constexpr int CG = C::CG;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sStage = smem;
+  // no room to align by hand; without static shared memory the base is aligned
+  extern __shared__ __align__(1024) uint8_t smem_aligned[];
+  if ((smem_u32(smem_aligned) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(p.status, STATUS_TIMEOUT);
+    return;
+  }
+  uint8_t* sStage = smem_aligned;
   uint8_t* sOut = sStage + C::STAGES * C::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_CHUNKS * C::CHUNK);
+  float* sScale = reinterpret_cast<float*>(sOut + C::OUT_CHUNKS * C::CHUNK);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sScale + C::SRING * (C::SCALES / 4));
   uint64_t* done = full + C::STAGES;
   uint64_t* tempty = done + C::STAGES;
   uint64_t* oready = tempty + C::NBUF;  // a tile's output is in shared memory
@@ -179,7 +199,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + CG);  // the loads, and each CTA's scales
       mbar_init(&done[s], 1);
     }
     for (int a = 0; a < C::NBUF; ++a) {
@@ -324,9 +344,83 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         }
         bulk_wait<0>();
       }
+    } else if (warp == C::SCALE_WARP) {
+      // ---------------------------------------------------------- scales
+      // The epilogue would have to wait for loads of its own (each k-block
+      // takes less time than one from L2), so this warp keeps four k-blocks'
+      // scales under way and puts them beside their stage.
+      int st = unit, skb = 0;
+      const float *px = nullptr, *pw = nullptr;  // of k-block 0
+      int rows = 0;
+      bool wlane = false;
+      auto seek = [&]() {
+        rows = 0;
+        wlane = false;
+        if (st >= num_tiles) return;
+        const int mb = st / p.tiles_n, nb = st - mb * p.tiles_n;
+        const int m = mb * C::TILE_M + static_cast<int>(rank) * C::BM + lane;
+        const int nblk = nb * (C::BN / 128) + lane;
+        rows = p.M - m;
+        wlane = lane < C::BN / 128 && nblk < p.n_blocks;
+        px = p.xs + m;
+        pw = p.ws + nblk;
+      };
+      auto load = [&](float (&v)[5]) {
+        const float* x = px + static_cast<size_t>(skb) * p.M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ld_scale(x + i * 32, rows > i * 32);
+        v[4] = ld_scale(pw + static_cast<size_t>(skb) * p.n_blocks, wlane);
+        if (++skb == num_kb) {
+          skb = 0;
+          st += nunits;
+          seek();
+        }
+      };
+      seek();
+      float v[4][5];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load(v[j]);
+      const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
+      // from here on a slot, or its stage's barrier, is not in its first round
+      constexpr int kFirst = C::SRING < C::STAGES ? C::SRING : C::STAGES;
+      const long long my_tiles = unit < num_tiles ? (num_tiles - unit + nunits - 1) / nunits : 0;
+      const long long steps = my_tiles * num_kb;
+      uint32_t stage = 0, slot = 0, wstage = kFirst - C::SRING + C::NBUF, wphase = 0;
+      bool ok = true;
+      for (long long g0 = 0; g0 < steps && ok; g0 += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (g0 + j >= steps) break;
+          if (g0 + j >= kFirst) {
+            if (!mbar_wait_inline(&done[wstage], wphase, w)) {
+              ok = false;
+              break;
+            }
+            if (++wstage == C::STAGES) {
+              wstage = 0;
+              wphase ^= 1u;
+            }
+          }
+          float* s = sScale + slot * (C::SCALES / 4);
+          if (++slot == C::SRING) slot = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[lane + i * 32] = v[j][i];
+          if (lane < C::BN / 128) s[128 + lane] = v[j][4];
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 1)
+              mbar_arrive(&full[stage]);
+            else
+              mbar_arrive_remote(full0 + stage * 8u);
+          }
+          load(v[j]);
+          if (++stage == C::STAGES) stage = 0;
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    // (scales: in place before the UMMAs of their stage were issued)
     if constexpr (C::SPLIT_REGS) reg_inc<C::REGS_EPI>();
     const int q = warp & 3;  // TMEM lane quarter
     const int e = warp - C::EPI0;
@@ -336,34 +430,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     const uint32_t orow = smem_u32(sOut) + (e >> 2) * (2 * C::CHUNK) + (q * 32 + lane) * 128;  // this thread's row, bf16
     const uint32_t qrow = smem_u32(sOut) + (C::BN / 64 + (e >> 2)) * C::CHUNK + (q * 32 + lane) * 128;  // codes
     const uint32_t xor16 = (lane & 7) << 4;  // of the 128-byte swizzle
-    uint32_t buf = 0, stage = 0, phase = 0, ofree_phase = 1;
-
-    // This thread's two scales, read two k-blocks ahead and across tiles: the
-    // next tile's first ones are under way while the current one is written.
-    int st = unit, skb = 0;
-    const float *px = nullptr, *pw = nullptr;
-    auto seek = [&]() {
-      px = pw = nullptr;
-      if (st >= num_tiles) return;
-      const int mb = st / p.tiles_n, nb = st - mb * p.tiles_n;
-      const int m = mb * C::TILE_M + static_cast<int>(rank) * C::BM + q * 32 + lane;
-      const int nblk = nb * (C::BN / 128) + (c0 >> 7);
-      if (m < p.M) px = p.xs + m;
-      if (nblk < p.n_blocks) pw = p.ws + nblk;
-    };
-    auto scales = [&](float& a, float& b) {
-      a = ld_scale(px + static_cast<size_t>(skb) * p.M, px != nullptr);
-      b = ld_scale(pw + static_cast<size_t>(skb) * p.n_blocks, pw != nullptr);
-      if (++skb == num_kb) {
-        skb = 0;
-        st += nunits;
-        seek();
-      }
-    };
-    seek();
-    float a0, b0, a1, b1;
-    scales(a0, b0);
-    scales(a1, b1);
+    uint32_t buf = 0, stage = 0, phase = 0, slot = 0, ofree_phase = 1;
 
     // this warp's rows of a chunk, out
     auto store_part = [&](const CUtensorMap* map, int chunk, int col, int row) {
@@ -383,11 +450,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
-        const float f = __fmul_rn(a0, b0);
-        const uint64_t f2 = f2_pack(f, f);
-        a0 = a1;
-        b0 = b1;
-        scales(a1, b1);
         if (!mbar_wait_inline(&done[stage], phase, w)) {
           ok = false;
           break;
@@ -397,6 +459,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         uint32_t v[2][16];
         const uint32_t src = tmem_mine + buf * C::BN;
         tmem_ld16_issue(src, v[0]);
+        const float* sc = sScale + slot * (C::SCALES / 4);
+        if (++slot == C::SRING) slot = 0;
+        const float f = __fmul_rn(sc[q * 32 + lane], sc[128 + (c0 >> 7)]);
+        const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           tmem_wait16(v[c & 1]);
