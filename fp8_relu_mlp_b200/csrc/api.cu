@@ -970,6 +970,12 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
 namespace {
 
 // ---- block-scaled FP8 products ----------------------------------------------
+int check_block_dims(int M, int a, int b) {
+  TRY(check_dims(M, a, b));
+  if (a > (1 << 22) || b > (1 << 22)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "widths must be <= 2^22");
+  return FP8MLP_OK;
+}
+
 int block_product(bool relu2, int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
                   const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di,
                   cudaStream_t stream) {
@@ -1026,7 +1032,7 @@ extern "C" {
 
 int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(M, K, 16));
+  TRY(check_block_dims(M, K, 16));
   if (M == 0) return FP8MLP_OK;
   REQUIRE_PTR(x);
   REQUIRE_PTR(xq);
@@ -1039,8 +1045,7 @@ int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* x
 int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t,
                                       float* ws_t, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(0, N, K));
-  if (N > (1 << 22) || K > (1 << 22)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "N and K must be <= 2^22");
+  TRY(check_block_dims(0, N, K));
   REQUIRE_PTR(W);
   if (Wq == nullptr && Wq_t == nullptr) return fail(FP8MLP_ERR_INVALID_ARG, "Wq and Wq_t are both NULL");
   if ((Wq == nullptr) != (ws == nullptr) || (Wq_t == nullptr) != (ws_t == nullptr))
@@ -1062,7 +1067,7 @@ int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* 
 int fp8mlp_linear_fwd_block(int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
                             const float* ws, uint16_t* y, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(M, N, K));
+  TRY(check_block_dims(M, N, K));
   if (M == 0) return FP8MLP_OK;
   REQUIRE_PTR(xq);
   REQUIRE_PTR4(xs);
@@ -1077,7 +1082,7 @@ int fp8mlp_linear_fwd_block(int M, int K, int N, const uint8_t* xq, const float*
 int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* Wq, const float* ws, uint8_t* xq,
                         float* xs, uint16_t* y, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(M, N, K));
+  TRY(check_block_dims(M, N, K));
   if (M == 0) return FP8MLP_OK;
   REQUIRE_PTR(x);
   REQUIRE_PTR(Wq);
@@ -1098,7 +1103,7 @@ int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* W
 int fp8mlp_up_proj_block(int M, int d, int h, const uint8_t* xq, const float* xs, const uint8_t* W1q,
                          const float* w1s, uint16_t* post, uint8_t* post_q, float* post_s, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(M, d, h));
+  TRY(check_block_dims(M, d, h));
   if (M == 0) return FP8MLP_OK;
   REQUIRE_PTR(xq);
   REQUIRE_PTR4(xs);
@@ -1116,7 +1121,7 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
                          const uint8_t* W2q_t, const float* w2s_t, uint8_t* xq, float* xs, uint16_t* post,
                          uint8_t* post_q, float* post_s, uint16_t* out, fp8mlp_stream_t stream) {
   g_detail.clear();
-  TRY(check_dims(M, d, h));
+  TRY(check_block_dims(M, d, h));
   if (M == 0) return FP8MLP_OK;
   REQUIRE_PTR(x);
   REQUIRE_PTR(W1q);

@@ -30,9 +30,11 @@ class AdamW:
         self.entries = []  # the tensors of each parameter: the descriptors hold their addresses
         self._descriptors = []
         self._plan = self._workspace = None
-        self.state = torch.zeros(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
+        self._addresses = set()
+        self.state = torch.empty(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
         self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
         self._coef = self.norm[1:]
+        self._settle()
         A.fp8mlp_adamw_state_init(self.state, lr, seed & 0xFFFFFFFF, step_count, stream)
 
     def add(self, grad, master=None, weight=None, weight_decay: float = 0.0, lr_mult: float = 1.0, state=None) -> dict:
@@ -63,24 +65,31 @@ class AdamW:
         if self.state_bits == 8 and not ("m_scale" in state and "v_scale" in state):
             raise ValueError("8-bit moments need m_scale and v_scale")
         e = dict(grad=grad, master=master, weight=weight, **state)
-        new = {t.data_ptr() for t in e.values() if t is not None and t.numel()}
-        if len(new) < sum(t is not None and t.numel() > 0 for t in e.values()) or new & {
-                t.data_ptr() for o in self.entries for t in o.values() if t is not None}:
+        given = [t.data_ptr() for t in e.values() if t is not None and t.numel()]
+        if len(set(given)) < len(given) or not self._addresses.isdisjoint(given):
             raise ValueError("a tensor is given twice: one step updates each weight once")
         self._descriptors.append(A.adamw_tensor(
             n, master, weight, grad, state["m"], state["v"], state.get("m_scale"), state.get("v_scale"), lr_mult,
             weight_decay, self.state_bits))
+        self._addresses.update(given)
         self.entries.append(e)
         self._plan = None
         return e
 
+    def _settle(self):
+        """Buffers are filled on the current stream; a step on a stream of its
+        own must not overtake that."""
+        if self.stream is not None:
+            torch.cuda.current_stream(self.device).synchronize()
+
     def set_lr(self, lr: float):
-        """For the steps from here on (a device write; also between replays of
-        a captured step)."""
+        """For the steps from here on (a device write on the current stream;
+        also between replays of a captured step)."""
         self.state[:1].view(torch.float32).fill_(lr)
 
     def step(self):
         if self._plan is None:
+            self._settle()
             self._plan = A.adamw_tensors(self._descriptors)
             if self.max_norm is not None:
                 self._workspace = torch.empty(A.fp8mlp_grad_norm_workspace_size(self._plan), dtype=torch.uint8,

@@ -487,7 +487,7 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
  * is computed from it is NaN.  Scales are fp32, block of the contraction
  * outermost: xs [ceil(K/128)][M], ws [ceil(K/128)][ceil(N/128)].  The last
  * group and the last weight blocks may be shorter.  4-byte alignment is
- * enough for the scales.
+ * enough for the scales.  Widths (K, N, d, h) <= 2^22.
  *   y[m,n] = bf16( sum_b fp32(xs[b,m] ws[b,n/128]) sum_{k in b} xq[m,k] Wq[n,k] )
  * with fp32 sums.  The gradient with respect to x is the same product over
  * the transposed cache, fp8mlp_linear_block(M, N, K, dY, Wq_t, ws_t, ...);
@@ -499,7 +499,7 @@ int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* x
 
 /* W [N,K] bf16 -> Wq [N,K] e4m3 with ws [ceil(K/128)][ceil(N/128)], and / or
  * the transposed Wq_t [K,N] with ws_t [ceil(N/128)][ceil(K/128)] (the same
- * codes and scales).  Either pair may be NULL, not both.  N, K <= 2^22. */
+ * codes and scales).  Either pair may be NULL, not both. */
 int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t,
                                       float* ws_t, fp8mlp_stream_t stream);
 

@@ -280,6 +280,25 @@ def test_another_stream_and_two_optimizers_at_once():
         assert all(torch.equal(x[k].view(U8), y[k].view(U8)) for k in x)
 
 
+def test_an_optimizer_on_a_stream_of_its_own_from_the_start():
+    # its buffers are zeroed on the current stream, which is kept busy here
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    g, w = torch.full((5000,), 0.5, device="cuda"), torch.zeros(5000, device="cuda")
+    for _ in range(20):
+        a = a @ a * 1e-3
+    opt = AdamW(state_bits=8, lr=1e-2, seed=9, step_count=6, max_norm=1.0, stream=side)
+    e = opt.add(g, master=w)
+    for _ in range(20):
+        a = a @ a * 1e-3
+    opt.step()
+    side.synchronize()
+    s = opt.state.clone()
+    torch.cuda.synchronize()
+    assert opt.read_state() == dict(lr=R.f32(1e-2), step=7, seed=9, skipped=0) and torch.equal(s, opt.state)
+    assert bool((w != 0).all()) and bool((e["v"].float() > 0).all())
+
+
 def test_state_carries_over():
     ts = tensors([999], 8, True)
     a, _ = build(ts, 8, True)

@@ -34,7 +34,7 @@ def test_block_products_refuse(name):
     fn, sizes, ptrs = BLOCK_CALLS[name]
     refused(INVALID, fn, -1, *sizes[1:], *ptrs)
     for i in range(1, len(sizes)):
-        for bad in (0, 8, 24, -16):
+        for bad in (0, 8, 24, -16, (1 << 22) + 16):
             refused(SHAPE, fn, *[bad if k == i else v for k, v in enumerate(sizes)], *ptrs)
     for i in range(len(ptrs)):
         refused(INVALID, fn, *sizes, *[None if k == i else v for k, v in enumerate(ptrs)])
