@@ -976,14 +976,20 @@ int check_block_dims(int M, int a, int b) {
   return FP8MLP_OK;
 }
 
+// few rows; x: bf16, quantised on the way, or NULL: from xq and xs
+int block_gemv(bool relu2, int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
+               const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di, cudaStream_t stream) {
+  const cudaError_t e = relu2 ? launch_block_gemv_up(M, K, N, x, xq, xs, Wq, ws, out, post_q, post_s, stream)
+                              : launch_block_gemv(M, K, N, x, xq, xs, Wq, ws, out, di->num_sms, stream);
+  return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, relu2 ? "up_proj_block launch" : "linear_fwd_block launch");
+}
+
 int block_product(bool relu2, int M, int K, int N, const uint8_t* xq, const float* xs, const uint8_t* Wq,
                   const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di,
                   cudaStream_t stream) {
-  if (!relu2 && block_gemv_fits(M, K, N)) {
-    const cudaError_t e = launch_block_gemv(M, K, N, nullptr, const_cast<uint8_t*>(xq), const_cast<float*>(xs), Wq, ws, out,
-                                            di->num_sms, stream);
-    return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "linear_fwd_block launch");
-  }
+  if (block_gemv_fits(relu2, M, K, N))
+    return block_gemv(relu2, M, K, N, nullptr, const_cast<uint8_t*>(xq), const_cast<float*>(xs), Wq, ws, out, post_q, post_s,
+                      di, stream);
   BlockGemmParams p{};
   const bool pairs = block_gemm_pairs(M, N, di->num_sms);
   TRY(map_kmajor(&p.tmA, xq, U8, 1, M, K, kGemmBM, "xq"));
@@ -1092,10 +1098,7 @@ int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* W
   REQUIRE_PTR(y);
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
-  if (block_gemv_fits(M, K, N)) {
-    const cudaError_t e = launch_block_gemv(M, K, N, x, xq, xs, Wq, ws, y, di->num_sms, stream);
-    return e == cudaSuccess ? FP8MLP_OK : cuda_fail(e, "linear_block launch");
-  }
+  if (block_gemv_fits(false, M, K, N)) return block_gemv(false, M, K, N, x, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
   TRY(quantize_rows(M, K, x, xq, xs, stream));
   return block_product(false, M, K, N, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
 }
@@ -1136,8 +1139,12 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
   REQUIRE_PTR(out);
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
-  TRY(quantize_rows(M, d, x, xq, xs, stream));
-  TRY(block_product(true, M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, di, stream));
+  if (block_gemv_fits(true, M, d, h)) {
+    TRY(block_gemv(true, M, d, h, x, xq, xs, W1q, w1s, post, post_q, post_s, di, stream));
+  } else {
+    TRY(quantize_rows(M, d, x, xq, xs, stream));
+    TRY(block_product(true, M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, di, stream));
+  }
   return block_product(false, M, h, d, post_q, post_s, W2q_t, w2s_t, out, nullptr, nullptr, di, stream);
 }
 

@@ -56,10 +56,12 @@ cudaError_t launch_block_gemm(bool relu2, bool pairs, BlockGemmParams& p, int nu
 
 // the product for few rows; x: bf16, quantised on the way (xq and xs are
 // written), or NULL: xq and xs are read
-constexpr int kGemvMaxM = 8;
-bool block_gemv_fits(int M, int K, int N);
+constexpr int kGemvMaxM = 8, kGemvMaxUp = 4;
+bool block_gemv_fits(bool relu2, int M, int K, int N);
 cudaError_t launch_block_gemv(int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
                               const float* ws, uint16_t* y, int num_sms, cudaStream_t s);
+cudaError_t launch_block_gemv_up(int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
+                                 const float* ws, uint16_t* post, uint8_t* post_q, float* post_s, cudaStream_t s);
 
 cudaError_t launch_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* xs, cudaStream_t s);
 cudaError_t launch_weight_block(int N, int K, const uint16_t* W, uint8_t* Wq, float* ws, uint8_t* Wq_t, float* ws_t,

@@ -150,7 +150,8 @@ def test_input_gradient_through_the_transposed_cache(M, K, N):
     assert abs(float(lhs - rhs)) <= float(slack)
 
 
-@pytest.mark.parametrize("M,d,h", [(1, 16, 16), (1, 768, 1024), (7, 144, 272), (16, 256, 144), (130, 128, 400),
+@pytest.mark.parametrize("M,d,h", [(1, 16, 16), (1, 768, 1024), (7, 144, 272), (2, 1040, 112), (3, 128, 144),
+                                   (4, 2320, 400), (5, 272, 656), (6, 16, 1040), (8, 512, 2064), (8, 4112, 48), (16, 256, 144), (130, 128, 400),
                                    (513, 272, 1040), (3000, 256, 2064)])
 def test_up_projection_and_mlp(M, d, h):
     x, W1, W2 = randn(M, M, d), randn(2, h, d, scale=d ** -0.5), randn(3, h, d, scale=h ** -0.5)
