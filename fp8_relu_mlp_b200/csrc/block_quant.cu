@@ -28,18 +28,25 @@ __global__ void __launch_bounds__(256) quantize_block_kernel(int M, int K, const
     v[g] = make_uint4(0, 0, 0, 0);
     if (row_ok && k < K) v[g] = *reinterpret_cast<const uint4*>(x + base + k);
   }
+  unsigned int top[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    unsigned int a = amax8(v[g]);
+    top[g] = amax8(v[g]);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    float inv;
-    const float s = block_scale(__uint_as_float(a << 16), &inv);
+    for (int o = 8; o > 0; o >>= 1) top[g] = max(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));
+  }
+  // lane g works out the scale of group g: two divisions for all of them
+  unsigned int mine = top[0];
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g) mine = sub == g ? top[g] : mine;
+  float inv;
+  const float s = block_scale(__uint_as_float(mine << 16), &inv);
+  if (row_ok && sub < kGroups && (kb0 + sub) * kBlock < K) xs[static_cast<size_t>(kb0 + sub) * M + m] = inv;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
     const int k = (kb0 + g) * kBlock + sub * 8;
-    if (row_ok && k < K) {
-      *reinterpret_cast<uint2*>(xq + base + k) = quant8(v[g], s);
-      if (sub == 0) xs[static_cast<size_t>(kb0 + g) * M + m] = inv;
-    }
+    const float sg = __shfl_sync(0xffffffffu, s, g, 16);
+    if (row_ok && k < K) *reinterpret_cast<uint2*>(xq + base + k) = quant8(v[g], sg);
   }
 }
 
