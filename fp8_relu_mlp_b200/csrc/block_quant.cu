@@ -7,7 +7,8 @@ namespace {
 
 using namespace dev;
 
-// x [M,K] bf16 -> codes and inverse scales of groups of 128 along K.  Sixteen
+// x [M,K] bf16 -> codes and inverse scales of groups of 128 along K.  HBM-bound:
+// 16384 x 768 in 6.5 us (5.8 TB/s), 8192 x 4096 in 15.2 (6.6).  Sixteen
 // lanes hold one group (16 bytes each), so its maximum takes four shuffles.
 // A half-warp walks kGroups groups of one row, all loads first: 64 bytes in
 // flight per thread keep HBM busy at 2048 threads per SM.
