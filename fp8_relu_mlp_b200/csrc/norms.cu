@@ -813,8 +813,7 @@ __global__ void __launch_bounds__(1024) norm_gate_bwd_sum_kernel(const NormGateB
     if (lane == 0) *p.dalpha = static_cast<float>(s);
   }
   if (job >= 2 && sp.groups > kBwdFewGroups) {
-    const int g = (job - 2) * 32 + row;
-    if (g < sp.groups && c < p.d)
+    for (int g = (job - 2) * 32 + row; g < sp.groups && c < p.d; g += 32 * (gridDim.y - 2))
       *reinterpret_cast<float2*>(p.dgate + static_cast<size_t>(g) * p.d + c) = gate_parts(p, sp, ws.gate, g, c, 0, 1);
     return;
   }
@@ -920,7 +919,7 @@ cudaError_t launch_norm_gate_bwd(const NormGateBwd& p, cudaStream_t s) {
   if (e != cudaSuccess || direct) return e;
   const bool one_gate = p.dgate != nullptr && sp.groups == 1;
   if (p.dw_pre == nullptr && p.dw_post == nullptr && !one_gate && !shared_gates && p.dalpha == nullptr) return e;
-  const int jobs = 2 + (!shared_gates ? 0 : sp.groups > kBwdFewGroups ? (sp.groups + 31) / 32 : sp.groups);
+  const int jobs = 2 + (!shared_gates ? 0 : sp.groups > kBwdFewGroups ? std::min((sp.groups + 31) / 32, 4096) : sp.groups);
   e = launch_pdl(norm_gate_bwd_sum_kernel, dim3((p.d + 63) / 64, jobs), dim3(1024), 0, s, p, sp);
   count_launches(1);
   return e;

@@ -293,6 +293,23 @@ def test_captured_replayed_and_on_another_stream():
         assert all(torch.equal(o[k], v) for k, v in {**want_f, **want_b}.items())
 
 
+def test_very_many_gate_rows():
+    # 2.2 million gate rows of 33: each is shared by several workers
+    M, d, rows = 33 * 2_200_000 + 5, 16, 33
+    y = torch.randn(M, d, generator=gen(1), device="cuda").to(BF)
+    g = torch.randn(R.cdiv(M, rows), d, generator=gen(2), device="cuda").to(BF)
+    dr_next = torch.randn(M, d, generator=gen(3), device="cuda").to(BF)
+    rpost = torch.rsqrt(y.float().square().mean(1) + EPS)
+    dr, dy, dgate = torch.empty_like(y), torch.empty_like(y), torch.full(g.shape, float("nan"), device="cuda")
+    ws = torch.empty(A.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows), dtype=U8, device="cuda")
+    A.fp8mlp_norm_gate_bwd(M, d, None, y, None, g, rows, None, rpost, None, None, None, None, dr_next, dr, dy, None, dgate,
+                           None, None, ws)
+    torch.cuda.synchronize()
+    t = dr_next[:-5].float() * (y[:-5].float() * rpost[:-5, None])
+    want, mag = t.view(-1, rows, d).sum(1), t.view(-1, rows, d).abs().sum(1)
+    assert bool(((dgate[:-1] - want).abs() <= ROW * mag).all()) and bool(torch.isfinite(dgate).all())
+
+
 def test_offsets_beyond_32_bits():
     M, d = 2 ** 31 // 768 + 700, 768
     p = dict(r=torch.empty(M, d, dtype=BF, device="cuda").fill_(0.5), y=torch.empty(M, d, dtype=BF, device="cuda").fill_(0.25))
