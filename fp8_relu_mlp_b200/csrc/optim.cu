@@ -32,7 +32,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kFew = 32, kMany = 256;  // descriptors per launch: as kernel arguments (at most 32764 bytes)
+constexpr int kFew = 64, kMany = 256;  // descriptors per launch: as kernel arguments (at most 32764 bytes)
 constexpr int kThreads = 256;
 constexpr int kStep = 8 * kThreads;  // elements a CTA takes at a time: two blocks of 128 per warp
 constexpr int kSms = 148;

@@ -219,6 +219,23 @@ def test_norm_below_the_limit_and_at_extremes():
     assert float(out[0]) == pytest.approx((0.25 * 300 * 301 / 2) ** 0.5, rel=2.0 ** -23) and float(out[1]) == 1.0
 
 
+@pytest.mark.parametrize("sizes", [[1], [3, 4, 5], [4096, 4097, 8191, 1], [1537] * 60, [0, 5000, 0, 1], [1 << 20], [(1 << 20) + 1],
+                                   [8193] * 127, [8193] * 128, [700] * 129, [0] * 200 + [9], [2359296] * 3 + [5]])
+def test_norm_against_float64(sizes):
+    g = torch.Generator(device="cuda").manual_seed(sum(sizes) + len(sizes))
+    gs = [torch.randn(n, generator=g, device="cuda") * torch.exp(4 * torch.randn(1, generator=g, device="cuda")) for n in sizes]
+    arr = A.adamw_tensors([A.adamw_tensor(x.numel(), None, None, x, None, None) for x in gs])
+    out, ws = torch.empty(2, device="cuda"), torch.empty(A.fp8mlp_grad_norm_workspace_size(arr), dtype=U8, device="cuda")
+    A.fp8mlp_grad_norm(arr, 0.25, out, ws)
+    want = float(sum(x.double().square().sum() for x in gs)) ** 0.5
+    # sums in double: the result's own rounding, one division and one sum
+    assert abs(float(out[0]) - want) <= 2.0 ** -23 * want
+    assert abs(float(out[1]) - min(1.0, 0.25 / (want + 1e-6))) <= 2.0 ** -21 * float(out[1])
+    again = torch.empty_like(out)
+    A.fp8mlp_grad_norm(arr, 0.25, again, ws)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_step_without_a_finite_norm_is_skipped(bad, bits):
