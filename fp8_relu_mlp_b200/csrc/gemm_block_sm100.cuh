@@ -114,7 +114,7 @@ __device__ __forceinline__ void reg_inc() {
 }
 
 // A load that stays where it is written: the compiler would sink a plain one
-// to its use, two k-blocks later, and put its latency back into the loop.
+// to its use, four k-blocks later, and put its latency back into the loop.
 __device__ __forceinline__ float ld_scale(const float* p, bool valid) {
   float v;
   asm volatile(

@@ -293,8 +293,8 @@ def test_offsets_beyond_32_bits():
     assert within(y[-100:], exact, mag, K + 8) and not y[:1000].any()
 
 
-def test_a_stalled_load_ends_with_a_status():
-    M, K, N = 300, 256, 256
+@pytest.mark.parametrize("M,K,N", [(300, 256, 256), (8000, 384, 1808)])
+def test_a_stalled_load_ends_with_a_status(M, K, N):
     x, W = randn(1, M, K), randn(2, N, K)
     Wq, ws, _, _ = weight(W)
     q, s = quantize(x)
