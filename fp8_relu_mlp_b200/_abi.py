@@ -170,7 +170,31 @@ def _find_current():
         return torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
 
     _current = plain if raw is None else fast
+    _find_marshal(torch)
     return True
+
+
+_marshal = None  # the compiled marshalling of the per-layer calls; set with _current
+
+
+def _find_marshal(torch):
+    """Sets ``_marshal`` where the module is built, for this very torch."""
+    global _marshal
+    try:
+        from . import _marshal as m
+    except ImportError:
+        return
+    if m.TORCH_VERSION != torch.__version__.split("+")[0]:
+        return
+    for name in m.names():
+        m.bind(name, ctypes.cast(getattr(lib, name), _p).value)
+    _marshal = m
+
+
+def _done(rc, name):
+    if rc != OK:
+        raise Fp8MlpError(rc, name)
+    return rc
 
 
 def _stream(s):
@@ -432,12 +456,17 @@ def _kblocks(n):
 
 
 def fp8mlp_quantize_block(M, K, x, xq, xs, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.quantize_block(M, K, x, xq, xs, stream), "fp8mlp_quantize_block")
     dev, raw = _here(stream)
     return _call("fp8mlp_quantize_block", M, K, _buf(x, 2 * M * K, "x", dev), _buf(xq, M * K, "xq", dev),
                  _buf(xs, 4 * M * _kblocks(K), "xs", dev), raw)
 
 
 def fp8mlp_weight_block_cache_refresh(N, K, W, Wq, ws, Wq_t=None, ws_t=None, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.weight_block_cache_refresh(N, K, W, Wq, ws, Wq_t, ws_t,
+                                                         stream), "fp8mlp_weight_block_cache_refresh")
     dev, raw = _here(stream)
     sc = 4 * _kblocks(K) * _kblocks(N)
     return _call("fp8mlp_weight_block_cache_refresh", N, K, _buf(W, 2 * N * K, "W", dev), _buf(Wq, N * K, "Wq", dev),
@@ -445,6 +474,8 @@ def fp8mlp_weight_block_cache_refresh(N, K, W, Wq, ws, Wq_t=None, ws_t=None, str
 
 
 def fp8mlp_linear_fwd_block(M, K, N, xq, xs, Wq, ws, y, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.linear_fwd_block(M, K, N, xq, xs, Wq, ws, y, stream), "fp8mlp_linear_fwd_block")
     dev, raw = _here(stream)
     kb = _kblocks(K)
     return _call("fp8mlp_linear_fwd_block", M, K, N, _buf(xq, M * K, "xq", dev), _buf(xs, 4 * M * kb, "xs", dev),
@@ -453,6 +484,8 @@ def fp8mlp_linear_fwd_block(M, K, N, xq, xs, Wq, ws, y, stream=None):
 
 
 def fp8mlp_linear_block(M, K, N, x, Wq, ws, xq, xs, y, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.linear_block(M, K, N, x, Wq, ws, xq, xs, y, stream), "fp8mlp_linear_block")
     dev, raw = _here(stream)
     kb = _kblocks(K)
     return _call("fp8mlp_linear_block", M, K, N, _buf(x, 2 * M * K, "x", dev), _buf(Wq, N * K, "Wq", dev),
@@ -461,6 +494,9 @@ def fp8mlp_linear_block(M, K, N, x, Wq, ws, xq, xs, y, stream=None):
 
 
 def fp8mlp_up_proj_block(M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.up_proj_block(M, d, h, xq, xs, W1q, w1s, post, post_q, post_s,
+                                            stream), "fp8mlp_up_proj_block")
     dev, raw = _here(stream)
     kd, kh = _kblocks(d), _kblocks(h)
     return _call("fp8mlp_up_proj_block", M, d, h, _buf(xq, M * d, "xq", dev), _buf(xs, 4 * M * kd, "xs", dev),
@@ -469,6 +505,9 @@ def fp8mlp_up_proj_block(M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, stream
 
 
 def fp8mlp_mlp_fwd_block(M, d, h, x, W1q, w1s, W2q_t, w2s_t, xq, xs, post, post_q, post_s, out, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.mlp_fwd_block(M, d, h, x, W1q, w1s, W2q_t, w2s_t, xq, xs, post, post_q, post_s, out,
+                                            stream), "fp8mlp_mlp_fwd_block")
     dev, raw = _here(stream)
     kd, kh = _kblocks(d), _kblocks(h)
     return _call("fp8mlp_mlp_fwd_block", M, d, h, _buf(x, 2 * M * d, "x", dev), _buf(W1q, h * d, "W1q", dev),
@@ -484,6 +523,9 @@ def _gate_rows(M, rows_per_gate):
 
 def fp8mlp_norm_gate_fwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, w_pre, eps, r_next, rstd_post, x, rstd_pre,
                          xq=None, xs=None, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.norm_gate_fwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, w_pre, eps, r_next,
+                                            rstd_post, x, rstd_pre, xq, xs, stream), "fp8mlp_norm_gate_fwd")
     dev, raw = _here(stream)
     n = 2 * M * d
     return _call("fp8mlp_norm_gate_fwd", M, d, _buf(r, n, "r", dev), _buf(y, n, "y", dev), _buf(w_post, 2 * d, "w_post", dev),
@@ -499,6 +541,10 @@ def fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate):
 
 def fp8mlp_norm_gate_bwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, rstd_post, r_next, w_pre, rstd_pre, dx,
                          dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, workspace, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.norm_gate_bwd(M, d, r, y, w_post, gate, rows_per_gate, alpha, rstd_post, r_next, w_pre,
+                                            rstd_pre, dx, dr_next, dr, dy, dw_post, dgate, dalpha, dw_pre, workspace,
+                                            stream), "fp8mlp_norm_gate_bwd")
     dev, raw = _here(stream)
     n, g = 2 * M * d, _gate_rows(M, rows_per_gate)
     need = int(lib.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows_per_gate))
@@ -548,6 +594,8 @@ def fp8mlp_grad_norm_workspace_size(tensors):
 
 
 def fp8mlp_grad_norm(tensors, max_norm, norm_coef, workspace, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.grad_norm(*_tensors(tensors), max_norm, norm_coef, workspace, stream), "fp8mlp_grad_norm")
     dev, raw = _here(stream)
     need = int(lib.fp8mlp_grad_norm_workspace_size(*_tensors(tensors)))
     return _call("fp8mlp_grad_norm", *_tensors(tensors), max_norm, _buf(norm_coef, 8, "norm_coef", dev),
@@ -555,6 +603,9 @@ def fp8mlp_grad_norm(tensors, max_norm, norm_coef, workspace, stream=None):
 
 
 def fp8mlp_adamw_step(tensors, st, state_bits, beta1, beta2, eps, grad_coef=None, stream=None):
+    if _marshal is not None:
+        return _done(_marshal.adamw_step(*_tensors(tensors), st, state_bits, beta1, beta2, eps, grad_coef, stream),
+                     "fp8mlp_adamw_step")
     dev, raw = _here(stream)
     return _call("fp8mlp_adamw_step", *_tensors(tensors), _buf(st, 32, "st", dev), state_bits, beta1, beta2, eps,
                  _buf(grad_coef, 4, "grad_coef", dev), raw)

@@ -4,7 +4,9 @@
 
 Every translation unit is compiled for ``sm_100a`` only, with -lineinfo and
 without fast-math (the scale arithmetic relies on IEEE division and sqrt).
-The CUDA runtime is linked statically; the driver's tensor-map encoder is
+Where torch and Python's headers are there, _marshal.so is built beside it
+with g++: the argument marshalling of the calls made per layer (without it
+the Python binding marshals them itself).  The CUDA runtime is linked statically; the driver's tensor-map encoder is
 reached through the runtime's driver entry-point query, so the library needs
 no libcuda at link time and can be loaded on a machine without a GPU.
 """
@@ -13,10 +15,12 @@ from __future__ import annotations
 import argparse
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8mlp.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "--expt-relaxed-constexpr",
@@ -56,8 +61,45 @@ def _digest() -> str:
     return h.hexdigest()[:16]
 
 
+def build_marshal(verbose: bool = False) -> str | None:
+    """_marshal.so, or None without torch, its headers, Python's or g++."""
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    python = sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    if spec is None or not cxx or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
+    torch = os.path.dirname(spec.origin)
+    header = os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")
+    if not os.path.exists(header) or not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return None
+    src = os.path.join(CSRC, "binding.cpp")
+    stamp = os.path.join(BUILD, "marshal.stamp")
+    h = hashlib.sha256()
+    for f in (src, __file__, os.path.join(torch, "version.py")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    h.update(" ".join((cxx, python, cuda, torch)).encode())
+    if os.path.exists(MARSHAL) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
+        return MARSHAL
+    tmp = MARSHAL + ".tmp"
+    lib = os.path.join(torch, "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + os.path.join(torch, "include"), "-I" + python, "-I" + cuda,
+           src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    with open(stamp, "w") as fh:
+        fh.write(h.hexdigest())
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_marshal(verbose)
     stamp = os.path.join(BUILD, "libfp8mlp.stamp")
     dg = _digest()
     if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == dg:

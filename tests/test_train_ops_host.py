@@ -14,6 +14,17 @@ F = 0x10000  # 16-byte aligned, never dereferenced on the host
 INVALID, SHAPE = A.ERR_INVALID_ARG, A.ERR_UNSUPPORTED_SHAPE
 
 
+@pytest.fixture(autouse=True, params=["python", "compiled"])
+def marshalling(request, monkeypatch):
+    if request.param == "python":
+        monkeypatch.setattr(A, "_marshal", None)
+    elif A._marshal is None:
+        monkeypatch.setattr(A, "_marshal", None)  # put back afterwards
+        A._find_marshal(torch)
+        if A._marshal is None:
+            pytest.skip("the module is not built")
+
+
 def refused(code, fn, *args):
     with pytest.raises(A.Fp8MlpError) as e:
         fn(*args, stream=0)
