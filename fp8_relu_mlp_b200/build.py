@@ -61,7 +61,7 @@ def _digest() -> str:
     return h.hexdigest()[:16]
 
 
-def build_marshal(verbose: bool = False) -> str | None:
+def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
     """_marshal.so, or None without torch, its headers, Python's or g++."""
     spec = importlib.util.find_spec("torch")  # found, not imported
     cxx = os.environ.get("CXX") or shutil.which("g++")
@@ -80,7 +80,7 @@ def build_marshal(verbose: bool = False) -> str | None:
         with open(f, "rb") as fh:
             h.update(fh.read())
     h.update(" ".join((cxx, python, cuda, torch)).encode())
-    if os.path.exists(MARSHAL) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
+    if not force and os.path.exists(MARSHAL) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
         return MARSHAL
     tmp = MARSHAL + ".tmp"
     lib = os.path.join(torch, "lib")
@@ -99,7 +99,7 @@ def build_marshal(verbose: bool = False) -> str | None:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    build_marshal(verbose)
+    build_marshal(force, verbose)
     stamp = os.path.join(BUILD, "libfp8mlp.stamp")
     dg = _digest()
     if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == dg:
