@@ -82,10 +82,19 @@ class AdamW:
         if self.stream is not None:
             torch.cuda.current_stream(self.device).synchronize()
 
+    def _finish(self):
+        """Steps on a stream of its own come to their end."""
+        if self.stream is not None:
+            s = self.stream if hasattr(self.stream, "synchronize") else torch.cuda.ExternalStream(self.stream, self.device)
+            s.synchronize()
+
     def set_lr(self, lr: float):
         """For the steps from here on (a device write on the current stream;
-        also between replays of a captured step)."""
+        also between replays of a captured step).  Waits for the steps before
+        where the optimizer has a stream of its own."""
+        self._finish()
         self.state[:1].view(torch.float32).fill_(lr)
+        self._settle()
 
     def step(self):
         if self._plan is None:
@@ -101,6 +110,7 @@ class AdamW:
         A.fp8mlp_adamw_step(self._plan, self.state, self.state_bits, *self.betas, self.eps, coef, self.stream)
 
     def read_state(self) -> dict:
+        self._finish()
         s = self.state.cpu()
         return dict(lr=float(s.view(torch.float32)[0]), step=int(s[1]), seed=int(s[2]) & 0xFFFFFFFF,
                     skipped=int(s[4]))

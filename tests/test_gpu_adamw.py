@@ -316,6 +316,33 @@ def test_an_optimizer_on_a_stream_of_its_own_from_the_start():
     assert bool((w != 0).all()) and bool((e["v"].float() > 0).all())
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_lr_and_state_with_a_stream_of_its_own(handle):
+    a = torch.randn(4096, 4096, device="cuda")
+    g, w = torch.full((3000,), 0.5, device="cuda"), torch.zeros(3000, device="cuda")
+    side = torch.cuda.Stream()
+    opt = AdamW(lr=1e-2, stream=side.cuda_stream if handle else side)
+    opt.add(g, master=w)
+    opt.step()
+    side.synchronize()
+    first = w.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):  # a step that waits behind other work
+        for _ in range(20):
+            a = a @ a * 1e-3
+    opt.step()
+    opt.set_lr(0.0)  # of the third step, not of the second
+    assert opt.read_state() == dict(lr=0.0, step=2, seed=0, skipped=0)
+    second = w.clone()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a = a @ a * 1e-3
+    opt.step()  # lr = 0 has arrived although the current stream is busy
+    assert opt.read_state()["step"] == 3
+    torch.cuda.synchronize()
+    assert bool((second < first).all()) and torch.equal(w, second)
+
+
 def test_state_carries_over():
     ts = tensors([999], 8, True)
     a, _ = build(ts, 8, True)
