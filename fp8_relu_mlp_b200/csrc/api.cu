@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -976,6 +977,30 @@ int check_block_dims(int M, int a, int b) {
   return FP8MLP_OK;
 }
 
+size_t cells(int rows, int cols, size_t each) { return static_cast<size_t>(rows) * static_cast<size_t>(cols) * each; }
+size_t scales(int rows_or_blocks, int K) { return cells(rows_or_blocks, cdiv(K, kBlock), 4); }
+
+struct Array {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+// A block of an output is written while others still read: what is written
+// shares no byte with what is read, nor with another output.
+int check_apart(std::initializer_list<Array> in, std::initializer_list<Array> out) {
+  auto meet = [](const Array& a, const Array& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x != 0 && y != 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+  };
+  for (const Array* o = out.begin(); o != out.end(); ++o) {
+    for (const Array& i : in)
+      if (meet(*o, i)) return fail(FP8MLP_ERR_INVALID_ARG, std::string(o->name) + " overlaps " + i.name);
+    for (const Array* q = o + 1; q != out.end(); ++q)
+      if (meet(*o, *q)) return fail(FP8MLP_ERR_INVALID_ARG, std::string(o->name) + " overlaps " + q->name);
+  }
+  return FP8MLP_OK;
+}
+
 // few rows; x: bf16, quantised on the way, or NULL: from xq and xs
 int block_gemv(bool relu2, int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
                const float* ws, uint16_t* out, uint8_t* post_q, float* post_s, const DeviceInfo* di, cudaStream_t stream) {
@@ -1043,6 +1068,7 @@ int fp8mlp_quantize_block(int M, int K, const uint16_t* x, uint8_t* xq, float* x
   REQUIRE_PTR(x);
   REQUIRE_PTR(xq);
   REQUIRE_PTR4(xs);
+  TRY(check_apart({{x, cells(M, K, 2), "x"}}, {{xq, cells(M, K, 1), "xq"}, {xs, scales(M, K), "xs"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   return quantize_rows(M, K, x, xq, xs, stream);
@@ -1064,6 +1090,8 @@ int fp8mlp_weight_block_cache_refresh(int N, int K, const uint16_t* W, uint8_t* 
     REQUIRE_PTR(Wq_t);
     REQUIRE_PTR4(ws_t);
   }
+  const size_t codes = cells(N, K, 1), sc = scales(cdiv(N, kBlock), K);
+  TRY(check_apart({{W, 2 * codes, "W"}}, {{Wq, codes, "Wq"}, {ws, sc, "ws"}, {Wq_t, codes, "Wq_t"}, {ws_t, sc, "ws_t"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   const cudaError_t e = launch_weight_block(N, K, W, Wq, ws, Wq_t, ws_t, stream);
@@ -1080,6 +1108,11 @@ int fp8mlp_linear_fwd_block(int M, int K, int N, const uint8_t* xq, const float*
   REQUIRE_PTR(Wq);
   REQUIRE_PTR4(ws);
   REQUIRE_PTR(y);
+  TRY(check_apart({{xq, cells(M, K, 1), "xq"},
+                   {xs, scales(M, K), "xs"},
+                   {Wq, cells(N, K, 1), "Wq"},
+                   {ws, scales(cdiv(N, kBlock), K), "ws"}},
+                  {{y, cells(M, N, 2), "y"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   return block_product(false, M, K, N, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
@@ -1096,6 +1129,8 @@ int fp8mlp_linear_block(int M, int K, int N, const uint16_t* x, const uint8_t* W
   REQUIRE_PTR(xq);
   REQUIRE_PTR4(xs);
   REQUIRE_PTR(y);
+  TRY(check_apart({{x, cells(M, K, 2), "x"}, {Wq, cells(N, K, 1), "Wq"}, {ws, scales(cdiv(N, kBlock), K), "ws"}},
+                  {{xq, cells(M, K, 1), "xq"}, {xs, scales(M, K), "xs"}, {y, cells(M, N, 2), "y"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   if (block_gemv_fits(false, M, K, N)) return block_gemv(false, M, K, N, x, xq, xs, Wq, ws, y, nullptr, nullptr, di, stream);
@@ -1115,6 +1150,11 @@ int fp8mlp_up_proj_block(int M, int d, int h, const uint8_t* xq, const float* xs
   REQUIRE_PTR(post);
   REQUIRE_PTR(post_q);
   REQUIRE_PTR4(post_s);
+  TRY(check_apart({{xq, cells(M, d, 1), "xq"},
+                   {xs, scales(M, d), "xs"},
+                   {W1q, cells(h, d, 1), "W1q"},
+                   {w1s, scales(cdiv(h, kBlock), d), "w1s"}},
+                  {{post, cells(M, h, 2), "post"}, {post_q, cells(M, h, 1), "post_q"}, {post_s, scales(M, h), "post_s"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   return block_product(true, M, d, h, xq, xs, W1q, w1s, post, post_q, post_s, di, stream);
@@ -1137,6 +1177,13 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
   REQUIRE_PTR(post_q);
   REQUIRE_PTR4(post_s);
   REQUIRE_PTR(out);
+  const size_t w = cells(h, d, 1), sc = scales(cdiv(h, kBlock), d);
+  const Array weights1 = {W1q, w, "W1q"}, scales1 = {w1s, sc, "w1s"}, weights2 = {W2q_t, w, "W2q_t"}, scales2 = {w2s_t, sc, "w2s_t"};
+  const Array codes = {xq, cells(M, d, 1), "xq"}, xsc = {xs, scales(M, d), "xs"}, full = {post, cells(M, h, 2), "post"};
+  const Array hidden = {post_q, cells(M, h, 1), "post_q"}, hsc = {post_s, scales(M, h), "post_s"};
+  TRY(check_apart({{x, cells(M, d, 2), "x"}, weights1, scales1, weights2, scales2}, {codes, xsc, full, hidden, hsc}));
+  // x has been read when out is written
+  TRY(check_apart({weights1, scales1, weights2, scales2, codes, xsc, full, hidden, hsc}, {{out, cells(M, d, 2), "out"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   if (block_gemv_fits(true, M, d, h)) {

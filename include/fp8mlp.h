@@ -491,7 +491,9 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
  *   y[m,n] = bf16( sum_b fp32(xs[b,m] ws[b,n/128]) sum_{k in b} xq[m,k] Wq[n,k] )
  * with fp32 sums.  The gradient with respect to x is the same product over
  * the transposed cache, fp8mlp_linear_block(M, N, K, dY, Wq_t, ws_t, ...);
- * the weight gradient stays BF16 (fp8mlp_linear_bwd).
+ * the weight gradient stays BF16 (fp8mlp_linear_bwd).  What a call writes may
+ * not overlap another of its arrays (FP8MLP_ERR_INVALID_ARG), except for
+ * fp8mlp_mlp_fwd_block's out, which may be x.
  * ------------------------------------------------------------------------ */
 
 /* x [M,K] bf16 -> xq [M,K] e4m3, xs [ceil(K/128)][M] fp32. */
@@ -544,7 +546,7 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
  * x = norm(r) w_pre); x = NULL leaves out the second (then w_pre, rstd_pre, xq
  * and xs are NULL); not both.  xq, xs (both or neither): x quantised
  * as by fp8mlp_quantize_block, rounded once from fp32.  r_next may equal r, x may
- * equal y.  d <= 8192.  eps finite and > 0.
+ * equal y; no other output may overlap an array of the call.  d <= 8192.  eps finite and > 0.
  * ------------------------------------------------------------------------ */
 int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
                          const uint16_t* gate, int rows_per_gate, const float* alpha, const uint16_t* w_pre, float eps,
@@ -560,7 +562,8 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
  *   dalpha = sum D r                                          (fp32)
  * y, dx and what belongs to them are NULL as in the forward (with y = NULL,
  * r_next is r and dr = D).  Any of dw_post, dgate, dalpha, dw_pre may be NULL;
- * r is read for dalpha only.  dr may equal dr_next, dy may equal y or dx.  The sums are taken
+ * r is read for dalpha only.  dr may equal dr_next, dy may equal y or dx; no
+ * other output may overlap an array of the call.  The sums are taken
  * in a fixed order.  M = 0 zeroes dw_post, dw_pre and dalpha.
  * workspace: fp8mlp_norm_gate_bwd_workspace_size bytes, no initial contents;
  * calls that may overlap on the GPU need workspaces of their own. */

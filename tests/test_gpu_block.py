@@ -330,3 +330,26 @@ def test_short_and_misplaced_buffers_are_refused():
         A.fp8mlp_linear_fwd_block(M, K, N, q, s, Wq, ws, y.cpu())
     with pytest.raises(A.Fp8MlpError, match="aligned"):
         A.fp8mlp_linear_fwd_block(M, K, N, q, s, Wq, ws, torch.empty(M * N + 1, dtype=BF, device="cuda")[1:])
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_the_mlp_may_write_over_its_input(M):
+    d, h = 144, 272
+    x, W1, W2 = randn(3, M, d), randn(4, h, d), randn(5, h, d)
+    W1q, w1s, _, _ = weight(W1)
+    _, _, W2q_t, w2s_t = weight(W2)
+
+    def run(out):
+        t = lambda r, c, dt: torch.empty(r, c, dtype=dt, device="cuda")  # noqa: E731
+        A.fp8mlp_mlp_fwd_block(M, d, h, src, W1q, w1s, W2q_t, w2s_t, t(M, d, U8), t(2, M, F32), t(M, h, BF), t(M, h, U8),
+                               t(3, M, F32), out)
+        torch.cuda.synchronize()
+        return out
+    src = x
+    want = run(torch.empty_like(x))
+    src = x.clone()
+    assert torch.equal(run(src), want)
+    with pytest.raises(A.Fp8MlpError, match="y overlaps x"):
+        sq = torch.zeros(M, d, dtype=BF, device="cuda")
+        A.fp8mlp_linear_block(M, d, d, sq, W1q[:d].contiguous(), w1s, torch.empty(M, d, dtype=U8, device="cuda"),
+                              torch.empty(2, M, device="cuda"), sq)

@@ -31,13 +31,16 @@ def refused(code, fn, *args):
     assert e.value.code == code, str(e.value)
 
 
+APART = [F * (i + 1) for i in range(11)]  # the largest array of these sizes has 32 KiB
 BLOCK_CALLS = {
-    "linear_fwd_block": (A.fp8mlp_linear_fwd_block, [4, 128, 256], [F] * 5),
-    "linear_block": (A.fp8mlp_linear_block, [4, 128, 256], [F] * 6),
-    "up_proj_block": (A.fp8mlp_up_proj_block, [4, 128, 256], [F] * 7),
-    "mlp_fwd_block": (A.fp8mlp_mlp_fwd_block, [4, 128, 256], [F] * 11),
-    "quantize_block": (A.fp8mlp_quantize_block, [4, 128], [F] * 3),
+    "linear_fwd_block": (A.fp8mlp_linear_fwd_block, [4, 128, 256], APART[:5]),
+    "linear_block": (A.fp8mlp_linear_block, [4, 128, 256], APART[:6]),
+    "up_proj_block": (A.fp8mlp_up_proj_block, [4, 128, 256], APART[:7]),
+    "mlp_fwd_block": (A.fp8mlp_mlp_fwd_block, [4, 128, 256], APART[:11]),
+    "quantize_block": (A.fp8mlp_quantize_block, [4, 128], APART[:3]),
 }
+OUTPUTS = {"linear_fwd_block": [4], "linear_block": [3, 4, 5], "up_proj_block": [4, 5, 6], "mlp_fwd_block": [5, 6, 7, 8, 9, 10],
+           "quantize_block": [1, 2]}
 
 
 @pytest.mark.parametrize("name", BLOCK_CALLS)
@@ -56,6 +59,27 @@ def test_block_products_refuse(name):
         refused(A.ERR_NO_DEVICE, fn, *sizes, *ptrs)
 
 
+@pytest.mark.parametrize("name", BLOCK_CALLS)
+def test_block_products_refuse_overlaps(name):
+    fn, sizes, ptrs = BLOCK_CALLS[name]
+    M, K = sizes[:2]
+    N = sizes[2] if len(sizes) > 2 else 0
+    size = {"linear_fwd_block": [M * K, 4 * M, N * K, 8, 2 * M * N], "linear_block": [2 * M * K, N * K, 8, M * K, 4 * M, 2 * M * N],
+            "up_proj_block": [M * K, 4 * M, N * K, 8, 2 * M * N, M * N, 8 * M], "quantize_block": [2 * M * K, M * K, 4 * M],
+            "mlp_fwd_block": [2 * M * K, N * K, 8, N * K, 8, M * K, 4 * M, 2 * M * N, M * N, 8 * M, 2 * M * K]}[name]
+    for o in OUTPUTS[name]:
+        for i in range(len(ptrs)):
+            if i == o or (name == "mlp_fwd_block" and {i, o} == {0, 10}):
+                continue
+            for at in (ptrs[i], ptrs[i] + (size[i] - 1) // 16 * 16, ptrs[i] - (size[o] - 1) // 16 * 16):
+                refused(INVALID, fn, *sizes, *[at if k == o else v for k, v in enumerate(ptrs)])
+            if not torch.cuda.is_available():  # side by side is no overlap
+                for at in (ptrs[i] + -(-size[i] // 16) * 16, ptrs[i] - -(-size[o] // 16) * 16):
+                    refused(A.ERR_NO_DEVICE, fn, *sizes, *[at if k == o else v for k, v in enumerate(ptrs)])
+    if name == "mlp_fwd_block" and not torch.cuda.is_available():
+        refused(A.ERR_NO_DEVICE, fn, *sizes, *ptrs[:-1], ptrs[0])
+
+
 def test_weight_cache_refuses():
     f = A.fp8mlp_weight_block_cache_refresh
     refused(SHAPE, f, 24, 16, F, F, F, F, F)
@@ -65,6 +89,11 @@ def test_weight_cache_refuses():
     refused(INVALID, f, 16, 16, F, F, None, None, None)
     refused(INVALID, f, 16, 16, F, F, F, F, None)
     refused(INVALID, f, 16, 16, F, F + 8, F, None, None)
+    far = [F * k for k in range(1, 6)]
+    for o in range(1, 5):
+        for i in range(5):
+            if i != o:
+                refused(INVALID, f, 16, 16, *[far[i] if k == o else v for k, v in enumerate(far)])
 
 
 FWD = dict(M=4, d=64, r=F, y=F, w_post=F, gate=F, rows_per_gate=2, alpha=F, w_pre=F, eps=1e-6, r_next=F, rstd_post=F, x=F,
