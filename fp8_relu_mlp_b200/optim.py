@@ -14,9 +14,13 @@ from __future__ import annotations
 import torch
 
 from . import _abi as A
+from ._order import as_stream, used_on
 
 
 class AdamW:
+    """Parameters may be added between steps; a step captured before goes on
+    with the parameters that it had."""
+
     def __init__(self, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8, seed: int = 0,
                  max_norm: float | None = None, step_count: int = 0, device="cuda", stream=None):
         if state_bits not in (32, 8):
@@ -30,6 +34,7 @@ class AdamW:
         self.entries = []  # the tensors of each parameter: the descriptors hold their addresses
         self._descriptors = []
         self._plan = self._workspace = None
+        self._outgrown = []  # workspaces that steps under way or captured ones may still use
         self._addresses = set()
         self.state = torch.empty(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
         self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
@@ -85,8 +90,7 @@ class AdamW:
     def _finish(self):
         """Steps on a stream of its own come to their end."""
         if self.stream is not None:
-            s = self.stream if hasattr(self.stream, "synchronize") else torch.cuda.ExternalStream(self.stream, self.device)
-            s.synchronize()
+            as_stream(self.stream, self.device).synchronize()
 
     def set_lr(self, lr: float):
         """For the steps from here on (a device write on the current stream;
@@ -96,13 +100,24 @@ class AdamW:
         self.state[:1].view(torch.float32).fill_(lr)
         self._settle()
 
+    def _replan(self):
+        self._plan = A.adamw_tensors(self._descriptors)
+        if self.max_norm is not None:
+            need = A.fp8mlp_grad_norm_workspace_size(self._plan)
+            if self._workspace is None or self._workspace.numel() < need:
+                if self._workspace is not None:
+                    self._outgrown.append(self._workspace)
+                    need = max(need, 2 * self._workspace.numel())
+                self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if self.stream is not None:
+            # freed while a step is under way, their memory waits for it
+            used_on(self.stream, self.device, [self.state, self.norm, self._workspace],
+                    *(e.values() for e in self.entries))
+
     def step(self):
         if self._plan is None:
+            self._replan()
             self._settle()
-            self._plan = A.adamw_tensors(self._descriptors)
-            if self.max_norm is not None:
-                self._workspace = torch.empty(A.fp8mlp_grad_norm_workspace_size(self._plan), dtype=torch.uint8,
-                                              device=self.device)
         coef = None
         if self.max_norm is not None:
             A.fp8mlp_grad_norm(self._plan, self.max_norm, self.norm, self._workspace, self.stream)

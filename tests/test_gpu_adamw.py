@@ -397,3 +397,36 @@ def test_offsets_beyond_32_bits():
         mq, ms = R.quant_state(m, (r & 0xFFFF).float() * 2.0 ** -16, False)
         assert torch.equal(e["m"][first:first + c].float(), mq)
         assert torch.equal(e["m_scale"][first // 128:first // 128 + ms.numel()], ms)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_parameters_added_between_steps_on_a_stream_of_its_own(handle):
+    # the first step still waits when the second's larger workspace is made and other tensors take what is free
+    a = torch.randn(4096, 4096, device="cuda")
+    n = [20000, 16384 * 300]
+    g = [torch.full((k,), 0.5 + i, device="cuda") for i, k in enumerate(n)]
+    w = [torch.zeros(k, device="cuda") for k in n]
+    side = torch.cuda.Stream()
+    opt = AdamW(lr=1e-2, max_norm=1.0, stream=side.cuda_stream if handle else side)
+    opt.add(g[0], master=w[0])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            a = a @ a * 1e-3
+    opt.step()
+    opt.add(g[1], master=w[1])
+    opt.step()
+    others = [torch.full((64,), float(i), device="cuda") for i in range(200)]
+    torch.cuda.synchronize()
+    assert all(bool((t == i).all()) for i, t in enumerate(others))
+    assert opt.read_state()["step"] == 2
+
+    def coef(k):  # of the first k gradients, in fp32 as the call works it out
+        norm = torch.tensor(sum(n[i] * (0.5 + i) ** 2 for i in range(k)), dtype=torch.float64).sqrt().float()
+        return norm, 1.0 / (norm + 1e-6)
+    assert float(opt.norm[0]) == float(coef(2)[0])
+    for i in range(2):
+        p = m = v = torch.zeros(1)
+        for t in range(1 + i, 3):
+            p, m, v = R.adamw(p, torch.tensor([0.5 + i]), m, v, t, 1e-2, 0.0, 0.9, 0.95, 1e-8, coef=float(coef(t)[1]))
+        assert bool((w[i].cpu() == p).all())

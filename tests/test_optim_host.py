@@ -1,0 +1,69 @@
+"""The optimizer's and the block-scaled stack's host side without a GPU: what is
+kept alive, and what waits for what.  The library's calls are recorded, not
+made."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+from fp8_relu_mlp_b200 import _abi as A
+from fp8_relu_mlp_b200.optim import AdamW
+
+
+class Stream:
+    """Stands in for torch.cuda.Stream."""
+
+    def __init__(self, log, handle):
+        self.log, self.cuda_stream = log, handle
+
+    def wait_stream(self, other):
+        self.log.append(("wait", (self.cuda_stream, other.cuda_stream)))
+
+    def synchronize(self):
+        self.log.append(("sync", (self.cuda_stream,)))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Library calls by name, with waits between them."""
+    log = []
+    for name in A._SIGS:
+        if hasattr(A, name):
+            monkeypatch.setattr(A, name, lambda *a, _n=name, **k: log.append((_n, a)))
+    monkeypatch.setattr(A, "adamw_tensor", lambda n, *a: A.AdamwTensor(n=n))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(log, 1))
+    return log
+
+
+def parameter(n):
+    return dict(grad=torch.zeros(n), master=torch.zeros(n))
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_a_workspace_outlives_the_steps_that_use_it(calls, own):
+    # a step under way, or captured, holds the workspace's address: a larger plan must not free it
+    opt = AdamW(max_norm=1.0, device="cpu", stream=Stream(calls, 2) if own else None)
+    opt.add(**parameter(100))
+    opt.step()
+    first = weakref.ref(opt._workspace)
+    opt.add(**parameter(1 << 18))
+    opt.step()
+    gc.collect()
+    assert first() is not None and opt._workspace.numel() >= 17 * 8
+    used = [a[3] for n, a in calls if n == "fp8mlp_grad_norm"]
+    assert [w.numel() for w in used] == [16, 17 * 8]
+    # they double, and a plan that fits takes the one there is
+    for outgrown in (2, 2, 2):
+        opt.add(**parameter(5))
+        opt.step()
+        assert len(opt._outgrown) == outgrown and opt._workspace.numel() == 2 * 17 * 8
+
+
+def test_without_a_stream_nothing_waits(calls):
+    opt = AdamW(device="cpu")
+    opt.add(**parameter(100))
+    opt.step()
+    opt.set_lr(0.5)
+    opt.read_state()
+    assert [c[0] for c in calls] == ["fp8mlp_adamw_state_init", "fp8mlp_adamw_step"]
