@@ -1,5 +1,6 @@
-"""A stream that an object of this package was given, next to torch's current
-one."""
+"""Order between torch's current stream and a stream that an object of this
+package was given: its buffers are filled, and its inputs written, on the
+current stream."""
 from __future__ import annotations
 
 import torch
@@ -7,7 +8,16 @@ import torch
 
 def as_stream(stream, device):
     """torch's form of a stream; an int is a handle."""
-    return stream if hasattr(stream, "synchronize") else torch.cuda.ExternalStream(stream, device)
+    return stream if hasattr(stream, "wait_stream") else torch.cuda.ExternalStream(stream, device)
+
+
+def after_current(stream, device):
+    """What is launched on ``stream`` from here on waits for the current
+    stream's work so far (by an event: the host does not wait, and both
+    streams may be in a graph capture)."""
+    s, current = as_stream(stream, device), torch.cuda.current_stream(device)
+    if s.cuda_stream != current.cuda_stream:
+        s.wait_stream(current)
 
 
 def used_on(stream, device, *groups):

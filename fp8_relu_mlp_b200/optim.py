@@ -14,12 +14,14 @@ from __future__ import annotations
 import torch
 
 from . import _abi as A
-from ._order import as_stream, used_on
+from ._order import after_current, as_stream, used_on
 
 
 class AdamW:
-    """Parameters may be added between steps; a step captured before goes on
-    with the parameters that it had."""
+    """With a ``stream`` of its own, what the optimizer launches waits for the
+    current stream's work so far; nothing waits for the optimizer but
+    ``set_lr`` and ``read_state``.  Parameters may be added between steps; a
+    step captured before goes on with the parameters that it had."""
 
     def __init__(self, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8, seed: int = 0,
                  max_norm: float | None = None, step_count: int = 0, device="cuda", stream=None):
@@ -85,7 +87,7 @@ class AdamW:
         """Buffers are filled on the current stream; a step on a stream of its
         own must not overtake that."""
         if self.stream is not None:
-            torch.cuda.current_stream(self.device).synchronize()
+            after_current(self.stream, self.device)
 
     def _finish(self):
         """Steps on a stream of its own come to their end."""
@@ -117,7 +119,7 @@ class AdamW:
     def step(self):
         if self._plan is None:
             self._replan()
-            self._settle()
+        self._settle()
         coef = None
         if self.max_norm is not None:
             A.fp8mlp_grad_norm(self._plan, self.max_norm, self.norm, self._workspace, self.stream)

@@ -430,3 +430,26 @@ def test_parameters_added_between_steps_on_a_stream_of_its_own(handle):
         for t in range(1 + i, 3):
             p, m, v = R.adamw(p, torch.tensor([0.5 + i]), m, v, t, 1e-2, 0.0, 0.9, 0.95, 1e-8, coef=float(coef(t)[1]))
         assert bool((w[i].cpu() == p).all())
+
+
+def test_a_first_step_captured_on_a_stream_of_its_own():
+    side = torch.cuda.Stream()
+    g, w = torch.full((5000,), 0.5, device="cuda"), torch.zeros(5000, device="cuda")
+    opt = AdamW(lr=1e-2, max_norm=1.0, stream=side)
+    opt.add(g, master=w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        opt.step()
+    assert opt.read_state()["step"] == 0
+    # the captured step goes on with its own parameter after another has come
+    extra = torch.zeros(1 << 18, device="cuda")
+    opt.add(torch.ones(1 << 18, device="cuda"), master=extra)
+    opt.step()
+    torch.cuda.synchronize()
+    after = extra.clone()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert opt.read_state()["step"] == 4 and torch.equal(after, extra) and bool((w < -3e-2).all())
+    assert float(opt.norm[0]) == pytest.approx(0.5 * 5000 ** 0.5, rel=2.0 ** -22)

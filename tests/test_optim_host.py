@@ -60,6 +60,21 @@ def test_a_workspace_outlives_the_steps_that_use_it(calls, own):
         assert len(opt._outgrown) == outgrown and opt._workspace.numel() == 2 * 17 * 8
 
 
+def test_a_step_waits_for_the_current_stream(calls):
+    opt = AdamW(max_norm=1.0, device="cpu", stream=Stream(calls, 2))
+    opt.add(**parameter(100))
+    for _ in range(2):
+        del calls[:]
+        opt.step()
+        assert [c[0] for c in calls] == ["wait", "fp8mlp_grad_norm", "fp8mlp_adamw_step"] and calls[0] == ("wait", (2, 1))
+    # in a capture the current stream is the optimizer's own: nothing to wait for, and no host wait that would end it
+    opt.stream = Stream(calls, 1)
+    opt.add(**parameter(100))
+    del calls[:]
+    opt.step()
+    assert [c[0] for c in calls] == ["fp8mlp_grad_norm", "fp8mlp_adamw_step"]
+
+
 def test_without_a_stream_nothing_waits(calls):
     opt = AdamW(device="cpu")
     opt.add(**parameter(100))
