@@ -20,6 +20,13 @@ def after_current(stream, device):
         s.wait_stream(current)
 
 
+def current_after(stream, device):
+    """What comes next on the current stream waits for ``stream``'s work so far."""
+    s, current = as_stream(stream, device), torch.cuda.current_stream(device)
+    if s.cuda_stream != current.cuda_stream:
+        current.wait_stream(s)
+
+
 def used_on(stream, device, *groups):
     """Tensors of ``groups`` that are freed go back to the allocator once
     ``stream`` has done what it was given until then."""

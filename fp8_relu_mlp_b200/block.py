@@ -17,6 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi as A
+from ._order import after_current, current_after, used_on
 
 
 class MLPBlock:
@@ -319,7 +320,12 @@ class BlockScaledStack:
     (BF16 [d]), ``gate`` (BF16), ``alpha`` (one fp32), one per layer.  Fill
     them, then ``refresh_caches()``, then ``optimizer()``, which takes its
     fp32 masters from them.  ``train_step`` (forward, backward, AdamW, caches)
-    launches only library calls, so it can be captured into a CUDA graph."""
+    launches only library calls, so it can be captured into a CUDA graph.
+
+    With a ``stream`` (a torch stream or a handle) every call is launched there
+    and waits for the current stream's work so far, i.e. for inputs and weights
+    copied on it; results are there for the current stream once it has waited
+    for ``stream``.  A capture is made on that stream."""
 
     def __init__(self, L: int, M: int, d: int, h: int, rows_per_gate: int | None = None, eps: float = 1e-6,
                  device="cuda", stream=None):
@@ -352,9 +358,18 @@ class BlockScaledStack:
         self.dgate, self.dalpha = each(G, d, dtype=f32, fill=0.0), each(1, dtype=f32)
         self.workspace = torch.empty(max(16, A.fp8mlp_norm_gate_bwd_workspace_size(M, d, self.rows)), dtype=u8,
                                      device=self.device)
+        if stream is not None:
+            used_on(stream, self.device, *(v if isinstance(v, list) else [v] for v in vars(self).values()
+                                           if isinstance(v, (list, torch.Tensor))))
+
+    def _begin(self):
+        """The buffers' fills, and what the caller copied into them, come first."""
+        if self.stream is not None:
+            after_current(self.stream, self.device)
 
     def refresh_caches(self):
         """FP8 weight caches from the current weights."""
+        self._begin()
         for l in range(self.L):
             A.fp8mlp_weight_block_cache_refresh(self.h, self.d, self.W1[l], self.W1q[l], self.w1s[l], stream=self.stream)
             A.fp8mlp_weight_block_cache_refresh(self.h, self.d, self.W2[l], None, None, self.W2q_t[l], self.w2s_t[l],
@@ -362,6 +377,7 @@ class BlockScaledStack:
 
     def forward(self):
         """``r[0]`` -> ``r[L]``."""
+        self._begin()
         M, d, h = self.M, self.d, self.h
         A.fp8mlp_norm_gate_fwd(M, d, self.r[0], None, None, None, 1, None, self.w_pre[0], self.eps, None, None, self.x[0],
                                self.rstd_pre[0], self.xq, self.xs, self.stream)
@@ -377,6 +393,7 @@ class BlockScaledStack:
 
     def backward(self):
         """``dr`` holds dL/dr_L on entry and dL/dr_0 on exit."""
+        self._begin()
         M, d, h = self.M, self.d, self.h
         for l in range(self.L - 1, -1, -1):
             # the norm of layer l + 1 (none behind the last) and the gate of layer l
@@ -396,6 +413,8 @@ class BlockScaledStack:
         ``masters=False`` keeps W1 and W2 in BF16 alone, rounded
         stochastically.  ``kw`` goes to AdamW (lr, betas, max_norm, ...)."""
         from .optim import AdamW
+        if self.stream is not None:
+            current_after(self.stream, self.device)  # earlier steps may still write the weights
         opt = AdamW(state_bits=state_bits, device=self.device, stream=self.stream, **kw)
         for l in range(self.L):
             for w, g in ((self.W1[l], self.dW1[l]), (self.W2[l], self.dW2[l])):

@@ -135,3 +135,63 @@ def test_steps_captured_and_eager_are_the_same(bits, masters):
         runs.append([t.clone() for k in ("W1", "W2", "w_pre", "w_post", "gate", "alpha", "r", "W1q", "W2q_t")
                      for t in getattr(s, k)] + [v for e in opt.entries for v in e.values() if v is not None])
     assert all(torch.equal(a.view(U8), b.view(U8)) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("handle,graph", [(False, False), (True, False), (False, True)])
+def test_a_stack_on_a_stream_of_its_own(handle, graph):
+    # weights and inputs are written on the current stream, which is busy while the calls are made
+    L, M, d, h, rows, steps = 2, 130, 256, 384, 50, 3
+    names = ("W1", "W2", "w_pre", "w_post", "gate", "alpha")
+    kw = dict(state_bits=8, weight_decay=0.1, lr=1e-2, max_norm=0.5, seed=5)
+    one = stack(L, M, d, h, rows, seed=7)
+    start = {k: [t.clone() for t in getattr(one, k)] for k in names}
+    r0, dr = one.r[0].clone(), one.dr.clone()
+    opt = one.optimizer(**kw)
+    for _ in range(steps):
+        one.r[0].copy_(r0)
+        one.dr.copy_(dr)
+        one.train_step(opt)
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+
+    def busy():
+        nonlocal a
+        for _ in range(10):
+            a = a @ a * 1e-3
+
+    side = torch.cuda.Stream()
+    busy()
+    two = BlockScaledStack(L, M, d, h, rows, stream=side.cuda_stream if handle else side)
+    for k in names:
+        for t, w in zip(getattr(two, k), start[k]):
+            t.copy_(w)
+    two.refresh_caches()
+    with torch.cuda.stream(side):
+        busy()  # the masters are taken behind this
+    opt2 = two.optimizer(**kw)
+
+    def step():
+        two.r[0].copy_(r0)
+        two.dr.copy_(dr)
+        two.train_step(opt2)
+
+    busy()
+    step()
+    torch.cuda.synchronize()  # the next copies overwrite what a step on another stream reads
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+        for _ in range(steps - 1):
+            g.replay()
+    else:
+        for _ in range(steps - 1):
+            busy()
+            step()
+            torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    assert opt2.read_state()["step"] == steps and A.fp8mlp_get_device_status() == 0
+    for k in names + ("r", "W1q", "W2q_t"):
+        assert all(torch.equal(x.view(U8), y.view(U8)) for x, y in zip(getattr(one, k), getattr(two, k))), k
+    for x, y in zip(opt.entries, opt2.entries):
+        assert all(torch.equal(x[k].view(U8), y[k].view(U8)) for k in x if x[k] is not None)

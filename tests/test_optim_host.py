@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from fp8_relu_mlp_b200 import _abi as A
+from fp8_relu_mlp_b200.block import BlockScaledStack
 from fp8_relu_mlp_b200.optim import AdamW
 
 
@@ -31,6 +32,7 @@ def calls(monkeypatch):
     for name in A._SIGS:
         if hasattr(A, name):
             monkeypatch.setattr(A, name, lambda *a, _n=name, **k: log.append((_n, a)))
+    monkeypatch.setattr(A, "fp8mlp_norm_gate_bwd_workspace_size", lambda *a: 16)
     monkeypatch.setattr(A, "adamw_tensor", lambda n, *a: A.AdamwTensor(n=n))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(log, 1))
     return log
@@ -82,3 +84,21 @@ def test_without_a_stream_nothing_waits(calls):
     opt.set_lr(0.5)
     opt.read_state()
     assert [c[0] for c in calls] == ["fp8mlp_adamw_state_init", "fp8mlp_adamw_step"]
+
+
+def test_the_stack_waits_for_its_fills_and_inputs(calls):
+    net = BlockScaledStack(2, 4, 32, 64, device="cpu", stream=Stream(calls, 2))
+    opt = None
+    for call in (net.refresh_caches, net.forward, net.backward, lambda: net.train_step(opt)):
+        del calls[:]
+        call()
+        assert calls[0] == ("wait", (2, 1)) and calls[1][0].startswith("fp8mlp_")
+        if opt is None:
+            del calls[:]
+            opt = net.optimizer()
+            # the weights are read on the current stream, behind steps that may still write them
+            assert calls[0] == ("wait", (1, 2))
+    net = BlockScaledStack(2, 4, 32, 64, device="cpu")
+    del calls[:]
+    net.train_step(net.optimizer())
+    assert not [c for c in calls if c[0] in ("wait", "sync")]
