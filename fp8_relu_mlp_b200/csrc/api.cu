@@ -978,6 +978,7 @@ int check_block_dims(int M, int a, int b) {
 }
 
 size_t cells(int rows, int cols, size_t each) { return static_cast<size_t>(rows) * static_cast<size_t>(cols) * each; }
+int gate_rows(int M, int rows) { return (M - 1) / rows + 1; }  // rows may be as large as an int gets
 size_t scales(int rows_or_blocks, int K) { return cells(rows_or_blocks, cdiv(K, kBlock), 4); }
 
 struct Array {
@@ -1230,6 +1231,20 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
   } else if (w_pre != nullptr || rstd_pre != nullptr || xq != nullptr) {
     return fail(FP8MLP_ERR_INVALID_ARG, "w_pre, rstd_pre, xq and xs go with x");
   }
+  const size_t full = cells(M, d, 2), gates = cells(gate_rows(M, rows_per_gate), d, 2), row = cells(1, d, 2), stat = cells(M, 1, 4);
+  // in place, an array is an output like another
+  TRY(check_apart({{r == r_next ? nullptr : r, full, "r"},
+                   {y == x ? nullptr : y, full, "y"},
+                   {w_post, row, "w_post"},
+                   {gate, gates, "gate"},
+                   {alpha, 4, "alpha"},
+                   {w_pre, row, "w_pre"}},
+                  {{r_next, full, "r_next"},
+                   {rstd_post, stat, "rstd_post"},
+                   {x, full, "x"},
+                   {rstd_pre, stat, "rstd_pre"},
+                   {xq, cells(M, d, 1), "xq"},
+                   {xs, scales(M, d), "xs"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   const NormGateFwd p{M, d, rows_per_gate, eps, r, y, w_post, gate, w_pre, alpha, r_next, x, rstd_post, rstd_pre, xq, xs};
@@ -1289,6 +1304,26 @@ int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, con
     return fail(FP8MLP_ERR_INVALID_ARG, "w_pre, rstd_pre and dw_pre go with dx");
   }
   REQUIRE_PTR(workspace);
+  const size_t full = cells(M, d, 2), gates = cells(gate_rows(M, rows_per_gate), d, 1), row = cells(1, d, 2), stat = cells(M, 1, 4);
+  // in place, an array is an output like another; r and r_next are read for dalpha and dx alone
+  TRY(check_apart({{dalpha != nullptr ? r : nullptr, full, "r"},
+                   {y == dy ? nullptr : y, full, "y"},
+                   {w_post, row, "w_post"},
+                   {gate, 2 * gates, "gate"},
+                   {alpha, 4, "alpha"},
+                   {rstd_post, stat, "rstd_post"},
+                   {dx != nullptr ? r_next : nullptr, full, "r_next"},
+                   {w_pre, row, "w_pre"},
+                   {rstd_pre, stat, "rstd_pre"},
+                   {dx == dy ? nullptr : dx, full, "dx"},
+                   {dr_next == dr ? nullptr : dr_next, full, "dr_next"}},
+                  {{dr, full, "dr"},
+                   {dy, full, "dy"},
+                   {dw_post, 2 * row, "dw_post"},
+                   {dgate, 4 * gates, "dgate"},
+                   {dalpha, 4, "dalpha"},
+                   {dw_pre, 2 * row, "dw_pre"},
+                   {workspace, norm_gate_bwd_workspace(M, d, rows_per_gate), "workspace"}}));
   DeviceInfo* di = nullptr;
   TRY(current_device(&di));
   const NormGateBwd p{M,  d,       rows_per_gate, r,  y,  w_post,  gate,  w_pre,  alpha,  rstd_post,

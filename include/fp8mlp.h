@@ -546,7 +546,8 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
  * x = norm(r) w_pre); x = NULL leaves out the second (then w_pre, rstd_pre, xq
  * and xs are NULL); not both.  xq, xs (both or neither): x quantised
  * as by fp8mlp_quantize_block, rounded once from fp32.  r_next may equal r, x may
- * equal y; no other output may overlap an array of the call.  d <= 8192.  eps finite and > 0.
+ * equal y; no other output may overlap an array of the call
+ * (FP8MLP_ERR_INVALID_ARG).  d <= 8192.  eps finite and > 0.
  * ------------------------------------------------------------------------ */
 int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
                          const uint16_t* gate, int rows_per_gate, const float* alpha, const uint16_t* w_pre, float eps,
@@ -563,8 +564,8 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
  * y, dx and what belongs to them are NULL as in the forward (with y = NULL,
  * r_next is r and dr = D).  Any of dw_post, dgate, dalpha, dw_pre may be NULL;
  * r is read for dalpha only.  dr may equal dr_next, dy may equal y or dx; no
- * other output may overlap an array of the call.  The sums are taken
- * in a fixed order.  M = 0 zeroes dw_post, dw_pre and dalpha.
+ * other output, nor the workspace, may overlap an array of the call
+ * (FP8MLP_ERR_INVALID_ARG).  The sums are taken in a fixed order.  M = 0 zeroes dw_post, dw_pre and dalpha.
  * workspace: fp8mlp_norm_gate_bwd_workspace_size bytes, no initial contents;
  * calls that may overlap on the GPU need workspaces of their own. */
 int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,

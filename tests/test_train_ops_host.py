@@ -228,3 +228,56 @@ def test_stochastic_rounding_of_the_plain_form():
         assert bool((s == 1).all())
         rest = q[torch.arange(n) % 128 != 0]
         assert set(rest.tolist()) <= {lo, hi} and abs(float(rest.mean()) - x) < 1e-3 * x + 2e-5
+
+
+# the norms' arrays apart from each other, their sizes, which ones are written, and the pairs that may be one array
+NORM_SIZES = dict(r=512, y=512, w_post=128, gate=256, alpha=4, w_pre=128, r_next=512, rstd_post=16, x=512, rstd_pre=16, xq=256,
+                  xs=16, dx=512, dr_next=512, dr=512, dy=512, dw_post=256, dgate=512, dalpha=4, dw_pre=256)
+NORM_CALLS = {
+    "fwd": (A.fp8mlp_norm_gate_fwd, FWD, ["r_next", "rstd_post", "x", "rstd_pre", "xq", "xs"], [("r_next", "r"), ("x", "y")]),
+    "bwd": (A.fp8mlp_norm_gate_bwd, BWD, ["dr", "dy", "dw_post", "dgate", "dalpha", "dw_pre", "workspace"],
+            [("dr", "dr_next"), ("dy", "y"), ("dy", "dx")])}
+
+
+@pytest.mark.parametrize("name", NORM_CALLS)
+def test_norms_refuse_overlaps(name):
+    fn, base, outputs, in_place = NORM_CALLS[name]
+    arrays = [k for k, v in base.items() if v == F]
+    far = 1 << 24
+    args = dict(base, **{k: far * (i + 1) for i, k in enumerate(arrays)})
+    size = dict(NORM_SIZES, workspace=A.fp8mlp_norm_gate_bwd_workspace_size(4, 64, 2))
+    cpu = not torch.cuda.is_available()  # a call that is in order would run
+    if cpu:
+        refused(A.ERR_NO_DEVICE, fn, *args.values())
+    for o in outputs:
+        for i in arrays:
+            if i == o:
+                continue
+            # the same place, all but the last 16 bytes apart, and side by side
+            for at in (args[i], args[i] + (size[i] - 1) // 16 * 16, args[i] - (size[o] - 1) // 16 * 16):
+                if at == args[i] and (o, i) in in_place:
+                    if cpu:
+                        refused(A.ERR_NO_DEVICE, fn, *{**args, o: at}.values())
+                else:
+                    refused(INVALID, fn, *{**args, o: at}.values())
+            if cpu:
+                for at in (args[i] + -(-size[i] // 16) * 16, args[i] - -(-size[o] // 16) * 16):
+                    refused(A.ERR_NO_DEVICE, fn, *{**args, o: at}.values())
+    for o, i in in_place:  # an array worked on in place is an output towards the others
+        for k in arrays:
+            if k != o and (o, k) not in in_place:
+                refused(INVALID, fn, *{**args, o: args[i], k: args[i]}.values())
+
+
+def test_norms_leave_unread_arrays_alone():
+    if torch.cuda.is_available():
+        pytest.skip("the calls would run")
+    args = dict(BWD, **{k: (i + 1) << 24 for i, k in enumerate(k for k, v in BWD.items() if v == F)})
+    # r is read for dalpha alone, r_next for dx
+    refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_bwd, *{**args, "dalpha": None, "r": args["dr"]}.values())
+    no_x = dict(dx=None, w_pre=None, rstd_pre=None, dw_pre=None)
+    refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_bwd, *{**args, **no_x, "r_next": args["dr"]}.values())
+    refused(INVALID, A.fp8mlp_norm_gate_bwd, *{**args, **no_x, "r": args["dr"]}.values())
+    no_y = dict(y=None, w_post=None, gate=None, alpha=None, rstd_post=None, dy=None, dw_post=None, dgate=None, dalpha=None)
+    refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_bwd, *{**args, **no_y}.values())
+    refused(INVALID, A.fp8mlp_norm_gate_bwd, *{**args, **no_y, "r_next": args["dr"]}.values())
