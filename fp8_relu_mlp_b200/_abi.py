@@ -94,6 +94,7 @@ _SIGS = {
     "fp8mlp_norm_gate_bwd": [_i, _i, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p],
     "fp8mlp_adamw_state_init": [_p, _f, _u32, _i, _p],
     "fp8mlp_grad_norm": [_i, _p, _f, _p, _p, _p],
+    "fp8mlp_adamw_check": [_i, _p, _p, _i, _p],
     "fp8mlp_adamw_step": [_i, _p, _p, _i, _f, _f, _f, _p, _p],
     "fp8mlp_get_device_status": [_p, _p],
     "fp8mlp_clear_device_status": [_p],
@@ -600,6 +601,11 @@ def fp8mlp_grad_norm(tensors, max_norm, norm_coef, workspace, stream=None):
     need = int(lib.fp8mlp_grad_norm_workspace_size(*_tensors(tensors)))
     return _call("fp8mlp_grad_norm", *_tensors(tensors), max_norm, _buf(norm_coef, 8, "norm_coef", dev),
                  _buf(workspace, need, "workspace", dev), raw)
+
+
+def fp8mlp_adamw_check(tensors, st, state_bits, grad_coef=None):
+    """What :func:`fp8mlp_adamw_step` refuses about its arrays, without a GPU."""
+    return _call("fp8mlp_adamw_check", *_tensors(tensors), _ptr(st), state_bits, _ptr(grad_coef))
 
 
 def fp8mlp_adamw_step(tensors, st, state_bits, beta1, beta2, eps, grad_coef=None, stream=None):

@@ -593,7 +593,7 @@ size_t fp8mlp_norm_gate_bwd_workspace_size(int M, int d, int rows_per_gate);
  *           rounded stochastically, and a positive sqrt(v) keeps at least
  *           the smallest code.  Zero codes with any finite scale start a state.
  *   lr_mult, weight_decay: the tensor's own factor of lr, and wd
- * No array may overlap another one of the call. */
+ * An array that is written may not overlap another one of the call. */
 typedef struct fp8mlp_adamw_tensor {
   int64_t n;
   float* p;
@@ -626,7 +626,8 @@ int fp8mlp_adamw_state_init(fp8mlp_adamw_state* st, float lr, uint32_t seed, int
  * norm_coef[1] = min(1, max_norm / (norm + 1e-6)), NaN if the norm is not
  * finite.  Reads n and g of each tensor.  max_norm > 0 (may be infinite).
  * workspace: fp8mlp_grad_norm_workspace_size bytes, 16-byte aligned, no
- * initial contents; calls that may overlap need workspaces of their own. */
+ * initial contents; calls that may overlap need workspaces of their own.
+ * norm_coef and workspace may not overlap each other nor a gradient. */
 int fp8mlp_grad_norm(int n_tensors, const fp8mlp_adamw_tensor* tensors, float max_norm, float* norm_coef,
                      void* workspace, fp8mlp_stream_t stream);
 size_t fp8mlp_grad_norm_workspace_size(int n_tensors, const fp8mlp_adamw_tensor* tensors);
@@ -636,9 +637,14 @@ size_t fp8mlp_grad_norm_workspace_size(int n_tensors, const fp8mlp_adamw_tensor*
  * nothing but st->skipped changes and FP8MLP_STATUS_STEP_SKIPPED is set.
  * state_bits 32 or 8.  0 <= beta < 1, eps > 0.  Random bits are a function of
  * st->seed, the step, the tensor's place in the call and the element's index.
- * Steps that share st run one after another. */
+ * Steps that share st run one after another.  Arrays that overlap are refused
+ * (FP8MLP_ERR_INVALID_ARG), st and grad_coef among them. */
 int fp8mlp_adamw_step(int n_tensors, const fp8mlp_adamw_tensor* tensors, fp8mlp_adamw_state* st, int state_bits,
                       float beta1, float beta2, float eps, const float* grad_coef, fp8mlp_stream_t stream);
+
+/* What fp8mlp_adamw_step refuses about its arrays, without a device. */
+int fp8mlp_adamw_check(int n_tensors, const fp8mlp_adamw_tensor* tensors, const fp8mlp_adamw_state* st, int state_bits,
+                       const float* grad_coef);
 
 /* ------------------------------------------------------------------------
  * Status and diagnostics

@@ -453,3 +453,25 @@ def test_a_first_step_captured_on_a_stream_of_its_own():
     torch.cuda.synchronize()
     assert opt.read_state()["step"] == 4 and torch.equal(after, extra) and bool((w < -3e-2).all())
     assert float(opt.norm[0]) == pytest.approx(0.5 * 5000 ** 0.5, rel=2.0 ** -22)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_overlapping_arrays_are_refused(bits):
+    ts = tensors([300, 5000], bits, True)
+    opt, raws = build(ts, bits, True, max_norm=1.0)
+    before = [r.clone() for r in raws]
+    norm = opt.norm.clone()
+    torch.cuda.synchronize()
+    arr = A.adamw_tensors(opt._descriptors)
+    arr[1].p = arr[0].g + 16
+    with pytest.raises(A.Fp8MlpError, match="overlaps") as e:
+        A.fp8mlp_adamw_step(arr, opt.state, bits, 0.9, 0.95, 1e-8)
+    assert e.value.code == A.ERR_INVALID_ARG
+    ws = torch.empty(A.fp8mlp_grad_norm_workspace_size(arr), dtype=U8, device="cuda")
+    with pytest.raises(A.Fp8MlpError, match="overlaps"):
+        A.fp8mlp_grad_norm(arr, 1.0, opt.entries[0]["grad"], ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, raws)) and torch.equal(norm, opt.norm)
+    assert opt.read_state()["step"] == 4
+    opt.step()
+    assert opt.read_state()["step"] == 5

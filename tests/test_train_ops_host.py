@@ -281,3 +281,103 @@ def test_norms_leave_unread_arrays_alone():
     no_y = dict(y=None, w_post=None, gate=None, alpha=None, rstd_post=None, dy=None, dw_post=None, dgate=None, dalpha=None)
     refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_bwd, *{**args, **no_y}.values())
     refused(INVALID, A.fp8mlp_norm_gate_bwd, *{**args, **no_y, "r_next": args["dr"]}.values())
+
+
+def descriptors(n=3, size=1000, flat=True, order=None):
+    """Tensors of ``size`` elements with arrays apart, as in flat buffers or one after another."""
+    names = ["p", "p_bf16", "g", "m", "v", "m_scale", "v_scale"]
+    out = []
+    for i in range(n) if order is None else order:
+        at = {k: ((j + 1) << 28) + (i << 16) if flat else ((i + 1) << 28) + (j << 16) for j, k in enumerate(names)}
+        out.append(dict(n=size, **at))
+    return out
+
+
+def adamw_array(ts):
+    return A.adamw_tensors([A.AdamwTensor(lr_mult=1.0, weight_decay=0.0, **t) for t in ts])
+
+
+ST, COEF = 1 << 40, (1 << 40) + 32
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("flat,order", [(True, None), (False, None), (True, [2, 0, 1]), (False, [1, 2, 0])])
+def test_adamw_refuses_overlaps(bits, flat, order):
+    def check(code, ts, st=ST, coef=COEF):
+        if code == A.OK:
+            assert A.fp8mlp_adamw_check(adamw_array(ts), st, bits, coef) == A.OK
+        else:
+            with pytest.raises(A.Fp8MlpError, match="overlaps") as e:
+                A.fp8mlp_adamw_check(adamw_array(ts), st, bits, coef)
+            assert e.value.code == code
+
+    def make():
+        return descriptors(3, 1000, flat, order)
+    check(A.OK, make())
+    check(A.OK, make(), coef=None)
+    size = dict(p=4000, p_bf16=2000, g=4000, m=1000 * bits // 8, v=1000 * bits // 8, m_scale=32, v_scale=32)
+    scales = ("m_scale", "v_scale")
+    for i in range(3):
+        for k in size:
+            for j in range(3):
+                for q in size:
+                    if (i, k) == (j, q):
+                        continue
+                    unread = bits == 32 and (k in scales or q in scales)
+                    harmless = unread or (k == "g" and q == "g")  # nothing is written there
+                    for shift in (0, (size[q] - 1) // 16 * 16, -((size[k] - 1) // 16 * 16)):
+                        ts = make()
+                        ts[i][k] = ts[j][q] + shift
+                        check(A.OK if harmless else INVALID, ts)
+                    for shift in (-(-size[q] // 16) * 16, -(-(-size[k] // 16) * 16)):  # side by side
+                        ts = make()
+                        ts[i][k] = ts[j][q] + shift
+                        check(A.OK, ts)
+            unread = bits == 32 and k in scales
+            ts = make()
+            ts[i][k] = ST
+            check(A.OK if unread else INVALID, ts)
+            ts[i][k] = COEF - 16
+            check(A.OK if unread else INVALID, ts)
+            ts[i][k] = COEF
+            check(A.OK if unread or k == "g" else INVALID, ts)
+    check(INVALID, make(), coef=ST + 8)
+    # empty tensors have no arrays
+    ts = make()
+    ts[1].update(n=0, p=ts[0]["p"], g=ts[0]["p"])
+    check(A.OK, ts)
+    ts[1].update(n=1)
+    check(INVALID, ts)
+
+
+def test_many_overlapping_arrays_are_found():
+    ts = descriptors(300, 1000)
+    assert A.fp8mlp_adamw_check(adamw_array(ts), ST, 8, COEF) == A.OK
+    ts.reverse()
+    assert A.fp8mlp_adamw_check(adamw_array(ts), ST, 8, COEF) == A.OK
+    # a gradient that spans others' (fine) and, behind them, a weight
+    ts[7]["n"] = 1000000
+    ts[7].update(g=1 << 50, p=(1 << 50) + (1 << 30), p_bf16=(1 << 51), m=1 << 52, v=1 << 53, m_scale=1 << 54, v_scale=1 << 55)
+    ts[8]["g"], ts[9]["g"], ts[10]["g"] = (1 << 50) + 16, (1 << 50) + 32, (1 << 50) + (1 << 20)
+    assert A.fp8mlp_adamw_check(adamw_array(ts), ST, 8, COEF) == A.OK
+    ts[11]["p"] = (1 << 50) + 3999984
+    with pytest.raises(A.Fp8MlpError, match="p of tensor 11 overlaps g of tensor 7"):
+        A.fp8mlp_adamw_check(adamw_array(ts), ST, 8, COEF)
+
+
+def test_adamw_check_refuses_what_the_step_refuses():
+    for t, st, bits in ((tensor(n=-1), F, 8), (tensor(m=None), F, 8), (tensor(), F, 16), (tensor(), None, 8), (tensor(), F + 8, 8)):
+        with pytest.raises(A.Fp8MlpError) as e:
+            A.fp8mlp_adamw_check(t, st, bits)
+        assert e.value.code == INVALID
+    assert A.fp8mlp_adamw_check(A.adamw_tensors([]), F, 8) == A.OK
+
+
+def test_gradient_norm_refuses_overlaps():
+    arr = adamw_array([dict(n=40000, g=1 << 20), dict(n=100, g=1 << 24), dict(n=0, g=1 << 28)])
+    out, ws = 1 << 28, 1 << 29
+    for bad in (dict(o=1 << 20), dict(o=(1 << 24) + 396), dict(w=(1 << 20) + 159984), dict(w=(1 << 20) - 16), dict(o=1 << 29)):
+        refused(INVALID, A.fp8mlp_grad_norm, arr, 1.0, bad.get("o", out), bad.get("w", ws))
+    if not torch.cuda.is_available():
+        refused(A.ERR_NO_DEVICE, A.fp8mlp_grad_norm, arr, 1.0, out, ws)
+        refused(A.ERR_NO_DEVICE, A.fp8mlp_grad_norm, arr, 1.0, (1 << 24) + 400, (1 << 20) - 48)
