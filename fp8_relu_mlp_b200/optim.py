@@ -11,6 +11,8 @@ device.
 """
 from __future__ import annotations
 
+from bisect import bisect, insort
+
 import torch
 
 from . import _abi as A
@@ -37,7 +39,7 @@ class AdamW:
         self._descriptors = []
         self._plan = self._workspace = None
         self._outgrown = []  # workspaces that steps under way or captured ones may still use
-        self._addresses = set()
+        self._extents = []  # first and last address of every tensor, in order
         self.state = torch.empty(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
         self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
         self._coef = self.norm[1:]
@@ -72,13 +74,18 @@ class AdamW:
         if self.state_bits == 8 and not ("m_scale" in state and "v_scale" in state):
             raise ValueError("8-bit moments need m_scale and v_scale")
         e = dict(grad=grad, master=master, weight=weight, **state)
-        given = [t.data_ptr() for t in e.values() if t is not None and t.numel()]
-        if len(set(given)) < len(given) or not self._addresses.isdisjoint(given):
-            raise ValueError("a tensor is given twice: one step updates each weight once")
+        given = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in e.values() if t is not None and t.numel())
+        known = self._extents
+        for k, x in enumerate(given):
+            i = bisect(known, x)
+            if ((k > 0 and given[k - 1][1] > x[0]) or (i > 0 and known[i - 1][1] > x[0]) or
+                    (i < len(known) and known[i][0] < x[1])):
+                raise ValueError("a tensor is given twice, or overlaps another: one step updates each weight once")
         self._descriptors.append(A.adamw_tensor(
             n, master, weight, grad, state["m"], state["v"], state.get("m_scale"), state.get("v_scale"), lr_mult,
             weight_decay, self.state_bits))
-        self._addresses.update(given)
+        for x in given:
+            insort(known, x)
         self.entries.append(e)
         self._plan = None
         return e

@@ -102,3 +102,26 @@ def test_the_stack_waits_for_its_fills_and_inputs(calls):
     del calls[:]
     net.train_step(net.optimizer())
     assert not [c for c in calls if c[0] in ("wait", "sync")]
+
+
+def test_tensors_that_overlap_are_refused(calls):
+    opt = AdamW(device="cpu")
+    flat = torch.zeros(10000)
+    opt.add(flat[:1000], master=flat[2000:3000])
+    opt.add(flat[1000:2000], master=flat[3000:4000])  # side by side
+    whole = flat[4000:9000]
+    for grad, master in ((whole[:500], flat[3999:4499]),  # by one element
+                         (flat[500:1500], whole[:1000]), (whole[:1000], whole[900:1900]), (whole[:1000], whole[:1000]),
+                         (flat[:10000], torch.zeros(10000)), (flat[10:20], whole[:10])):
+        with pytest.raises(ValueError, match="overlap"):
+            opt.add(grad, master=master)
+    with pytest.raises(ValueError, match="overlap"):
+        opt.add(whole[:100], master=whole[100:200], state=dict(m=whole[200:300], v=whole[250:350]))
+    with pytest.raises(ValueError, match="overlap"):
+        opt.add(whole[:100], master=whole[100:200], weight=whole[200:250].view(torch.bfloat16),
+                state=dict(m=whole[249:349], v=whole[400:500]))
+    # what was refused left nothing behind
+    assert len(opt.entries) == len(opt._descriptors) == 2
+    opt.add(whole[:100], master=whole[100:200], weight=whole[200:250].view(torch.bfloat16),
+            state=dict(m=whole[250:350], v=whole[400:500]))
+    opt.add(flat[:0], master=flat[:0])
