@@ -35,6 +35,7 @@ class AdamW:
             raise ValueError("betas must be in [0, 1) and eps > 0")
         self.state_bits, self.betas, self.eps, self.max_norm = state_bits, tuple(betas), eps, max_norm
         self.device, self.stream = torch.device(device), stream
+        self._moments = (torch.float32,) if state_bits == 32 else (torch.float8_e4m3fn, torch.uint8)  # codes as bytes too
         self.entries = []  # the tensors of each parameter: the descriptors hold their addresses
         self._descriptors = []
         self._plan = self._workspace = None
@@ -68,11 +69,13 @@ class AdamW:
                 state = {k: torch.zeros(n, dtype=torch.float8_e4m3fn, device=grad.device) for k in ("m", "v")}
                 state.update({k: torch.ones(-(-n // 128), dtype=torch.float32, device=grad.device)
                               for k in ("m_scale", "v_scale")})
-        size = self.state_bits // 8
-        if state["m"].element_size() != size or state["v"].element_size() != size:
-            raise ValueError(f"the moments must have {self.state_bits} bits")
-        if self.state_bits == 8 and not ("m_scale" in state and "v_scale" in state):
-            raise ValueError("8-bit moments need m_scale and v_scale")
+        if state["m"].dtype not in self._moments or state["v"].dtype not in self._moments:
+            raise ValueError(f"the moments must have {self.state_bits} bits: {' or '.join(map(str, self._moments))}")
+        if self.state_bits == 8:
+            if state.get("m_scale") is None or state.get("v_scale") is None:
+                raise ValueError("8-bit moments need m_scale and v_scale")
+            if state["m_scale"].dtype != torch.float32 or state["v_scale"].dtype != torch.float32:
+                raise ValueError("m_scale and v_scale must be fp32")
         e = dict(grad=grad, master=master, weight=weight, **state)
         given = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in e.values() if t is not None and t.numel())
         known = self._extents

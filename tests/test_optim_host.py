@@ -125,3 +125,23 @@ def test_tensors_that_overlap_are_refused(calls):
     opt.add(whole[:100], master=whole[100:200], weight=whole[200:250].view(torch.bfloat16),
             state=dict(m=whole[250:350], v=whole[400:500]))
     opt.add(flat[:0], master=flat[:0])
+
+
+@pytest.mark.parametrize("bits,moments,scales", [
+    (8, torch.float8_e5m2, torch.float32), (8, torch.int8, torch.float32), (8, torch.bool, torch.float32),
+    (8, torch.float8_e4m3fn, torch.float64), (8, torch.uint8, torch.int32), (8, torch.uint8, None),
+    (32, torch.int32, None), (32, torch.float64, None), (32, torch.float8_e4m3fn, None)])
+@pytest.mark.parametrize("both", [False, True])
+def test_states_of_another_type_are_refused(calls, bits, moments, scales, both):
+    right = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    opt = AdamW(state_bits=bits, device="cpu")
+    wrong = dict(m=torch.zeros(256, dtype=moments), v=torch.zeros(256, dtype=moments if both else right))
+    if scales is not None:
+        wrong.update(m_scale=torch.ones(2, dtype=scales if both else torch.float32), v_scale=torch.ones(2, dtype=scales))
+    with pytest.raises(ValueError, match="moments must|m_scale"):
+        opt.add(**parameter(256), state=wrong)
+    good = {k: torch.zeros(256, dtype=right) for k in ("m", "v")}
+    if bits == 8:
+        good.update({k: torch.ones(2) for k in ("m_scale", "v_scale")})
+        good["m"] = good["m"].view(torch.uint8)
+    opt.add(**parameter(256), state=good)
