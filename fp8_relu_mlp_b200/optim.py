@@ -11,6 +11,7 @@ device.
 """
 from __future__ import annotations
 
+import math
 from bisect import bisect, insort
 
 import torch
@@ -108,6 +109,8 @@ class AdamW:
         """For the steps from here on (a device write on the current stream;
         also between replays of a captured step).  Waits for the steps before
         where the optimizer has a stream of its own."""
+        if not isinstance(lr, torch.Tensor) and not math.isfinite(lr):
+            raise ValueError("lr must be finite")
         self._finish()
         self.state[:1].view(torch.float32).fill_(lr)
         self._settle()

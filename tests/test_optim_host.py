@@ -145,3 +145,12 @@ def test_states_of_another_type_are_refused(calls, bits, moments, scales, both):
         good.update({k: torch.ones(2) for k in ("m_scale", "v_scale")})
         good["m"] = good["m"].view(torch.uint8)
     opt.add(**parameter(256), state=good)
+
+
+@pytest.mark.parametrize("lr", [float("nan"), float("inf"), -float("inf")])
+def test_a_rate_that_is_not_finite_is_refused(calls, lr):
+    opt = AdamW(device="cpu")
+    opt.set_lr(0.25)
+    with pytest.raises(ValueError, match="finite"):
+        opt.set_lr(lr)
+    assert opt.read_state()["lr"] == 0.25
