@@ -4,9 +4,10 @@
 
 Every translation unit is compiled for ``sm_100a`` only, with -lineinfo and
 without fast-math (the scale arithmetic relies on IEEE division and sqrt).
-Where torch and Python's headers are there, _marshal.so is built beside it
-with g++: the argument marshalling of the calls made per layer (without it
-the Python binding marshals them itself).  The CUDA runtime is linked statically; the driver's tensor-map encoder is
+Where torch and Python's headers are there, the module _marshal is built beside
+it with g++: the argument marshalling of the calls made per layer.  Without it
+the Python binding marshals them itself, so a module that cannot be built is a
+warning, and a stale one is removed.  The CUDA runtime is linked statically; the driver's tensor-map encoder is
 reached through the runtime's driver entry-point query, so the library needs
 no libcuda at link time and can be loaded on a machine without a GPU.
 """
@@ -21,6 +22,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,7 +31,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8mlp.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+# named for this Python alone: torch's version is all that the binding compares
+MARSHAL = os.path.join(PKG, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+UNTAGGED = os.path.join(PKG, "_marshal.so")
+# what binding.cpp includes, under torch's include folder
+TORCH_HEADERS = ("c10/cuda/CUDAFunctions.h", "c10/cuda/CUDAStream.h", "torch/csrc/autograd/python_variable.h",
+                 "torch/headeronly/version.h")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", "--expt-relaxed-constexpr",
@@ -61,36 +68,58 @@ def _digest() -> str:
     return h.hexdigest()[:16]
 
 
-def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
-    """_marshal.so, or None without torch, its headers, Python's or g++."""
-    spec = importlib.util.find_spec("torch")  # found, not imported
+def _marshal_command(torch: str) -> list[str] | None:
+    """How to build the module, but for its output; None where something is missing."""
     cxx = os.environ.get("CXX") or shutil.which("g++")
-    python = sysconfig.get_paths()["include"]
-    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    if spec is None or not cxx or not os.path.exists(os.path.join(python, "Python.h")):
+    python, include, lib = sysconfig.get_paths()["include"], os.path.join(torch, "include"), os.path.join(torch, "lib")
+    try:
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    except RuntimeError:
+        return None
+    needed = [os.path.join(include, h) for h in TORCH_HEADERS]
+    needed += [os.path.join(python, "Python.h"), os.path.join(cuda, "cuda_runtime_api.h"), os.path.join(lib, "libc10_cuda.so")]
+    if not cxx or not all(os.path.exists(f) for f in needed):
+        return None
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + include, "-I" + python, "-I" + cuda,
+            os.path.join(CSRC, "binding.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _remove(path: str):
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
+    """The module's path, or None where it cannot be built."""
+    _remove(UNTAGGED)  # any Python would load it
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    if spec is None or not spec.origin:
         return None
     torch = os.path.dirname(spec.origin)
-    header = os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")
-    if not os.path.exists(header) or not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
-        return None
-    src = os.path.join(CSRC, "binding.cpp")
     stamp = os.path.join(BUILD, "marshal.stamp")
     h = hashlib.sha256()
-    for f in (src, __file__, os.path.join(torch, "version.py")):
+    for f in (os.path.join(CSRC, "binding.cpp"), __file__, os.path.join(torch, "version.py")):
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join((cxx, python, cuda, torch)).encode())
+    h.update(MARSHAL.encode())
     if not force and os.path.exists(MARSHAL) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
         return MARSHAL
+    _remove(MARSHAL)
+    cmd = _marshal_command(torch)
+    if cmd is None:
+        return None
     tmp = MARSHAL + ".tmp"
-    lib = os.path.join(torch, "lib")
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + os.path.join(torch, "include"), "-I" + python, "-I" + cuda,
-           src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    cmd += ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stdout + r.stderr if r.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is not None:
+        warnings.warn(f"the argument marshalling stays in Python: {cmd[0]} failed on binding.cpp:\n{failed}")
+        return None
     os.replace(tmp, MARSHAL)
     with open(stamp, "w") as fh:
         fh.write(h.hexdigest())
@@ -99,7 +128,12 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    lib = build_library(force, verbose, extra)
     build_marshal(force, verbose)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     stamp = os.path.join(BUILD, "libfp8mlp.stamp")
     dg = _digest()
     if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == dg:
