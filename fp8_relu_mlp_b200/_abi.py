@@ -419,14 +419,21 @@ def _here(stream):
     dev, raw = (_current or _no_gpu)()
     if stream is None:
         return dev, raw
-    return dev, stream if stream.__class__ is int else stream.cuda_stream
+    return dev, _address(stream if stream.__class__ is int else stream.cuda_stream, "stream")
+
+
+def _address(v, name):
+    """An int that ctypes would cut to 64 bits is refused."""
+    if v.__class__ is int and not -(1 << 63) <= v < 1 << 64:
+        raise OverflowError(f"{name}: an address has 64 bits")
+    return v
 
 
 def _buf(t, need, name, dev):
     """Device address of ``t`` with at least ``need`` bytes on device ``dev``
     (None stays NULL; an int is an address the caller vouches for)."""
     if t is None or t.__class__ is int:
-        return t
+        return _address(t, name)
     try:
         ok = t.is_contiguous() and t.nbytes >= need and t.get_device() == dev
     except AttributeError:

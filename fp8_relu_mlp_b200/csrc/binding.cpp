@@ -97,6 +97,14 @@ struct Args {
     if (v == -1.0 && PyErr_Occurred()) ok = false;
     return static_cast<float>(v);
   }
+  void* address(PyObject* o, const char* name) {
+    void* p = PyLong_AsVoidPtr(o);
+    if (p == nullptr && PyErr_Occurred()) {
+      ok = false;
+      if (PyErr_ExceptionMatches(PyExc_OverflowError)) PyErr_Format(PyExc_OverflowError, "%s: an address has 64 bits", name);
+    }
+    return p;
+  }
   // device address of a tensor with at least `need` bytes (None: NULL; an int
   // is an address the caller vouches for)
   template <class T = void>
@@ -121,8 +129,7 @@ struct Args {
       }
       ok = false;
     } else if (PyLong_CheckExact(o)) {
-      p = PyLong_AsVoidPtr(o);
-      if (p == nullptr && PyErr_Occurred()) ok = false;
+      p = address(o, name);
     } else {
       PyErr_Format(PyExc_TypeError, "%s: cannot pass %R as a pointer", name, reinterpret_cast<PyObject*>(Py_TYPE(o)));
       ok = false;
@@ -134,15 +141,14 @@ struct Args {
     if (!ok) return nullptr;
     PyObject* o = a[i++];
     if (o == Py_None) return dev >= 0 ? c10::cuda::getCurrentCUDAStream().stream() : nullptr;
-    if (PyLong_CheckExact(o)) return PyLong_AsVoidPtr(o);
+    if (PyLong_CheckExact(o)) return address(o, "stream");
     PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
     if (h == nullptr) {
       ok = false;
       return nullptr;
     }
-    void* s = PyLong_AsVoidPtr(h);
+    void* s = address(h, "stream");
     Py_DECREF(h);
-    if (s == nullptr && PyErr_Occurred()) ok = false;
     return s;
   }
 };

@@ -132,3 +132,21 @@ def test_another_torch_is_left_alone(both, monkeypatch):
     both(False)
     A._find_marshal(Torch)
     assert A._marshal is None
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("v", [1 << 70, 1 << 64, -(1 << 63) - 1])
+def test_addresses_beyond_64_bits_are_refused(name, v, both):
+    fn = getattr(A, "fp8mlp_" + name)
+    args = arguments(name, lambda i: 0x10000)
+
+    class Stream:
+        cuda_stream = v
+    pointers = [k for k, a in args.items() if a == 0x10000 and k != "stream"]
+    for change in [dict(stream=v), dict(stream=Stream())] + [{k: v} for k in pointers]:
+        got = []
+        for way in (True, False):
+            both(way)
+            got.append(outcome(fn, **{**args, "stream": 0, **change}))
+        assert got[0] == got[1] and got[0][0] is OverflowError, change
+        assert got[0][1].startswith(next(iter(change)))
