@@ -370,19 +370,29 @@ __global__ void __launch_bounds__(CTA ? 384 : 512) norm_gate_fwd_kernel(const No
 // run's rows in turn, so that what is in flight lies close together: a run
 // per worker instead, 14 rows of 768, took 51 us where this takes 37
 // (16384 x 768), as HBM then opens a page for each worker.  Larger teams share
-// more gate rows: a worker leaves one part per gate row of its team's run.
+// more gate rows: a worker leaves one part per gate row of its team's run, or
+// per row where gate rows are no longer than the team.  Short gate rows are
+// dealt whole and leave no parts.
 struct NormBwdSplit {
   int ctas, groups;  // gate rows
   int rpg;           // rows per gate row, at most M
   int team, run;     // workers per team, rows per team
   int unit;          // neighbouring rows dealt at once: 1, or a whole gate row
-  int slots;         // parts of gate rows per worker: of the most that a run touches
+  int slots;         // parts of gate rows per worker: of the most that it can touch
+  bool by_row;       // 1: each of a worker's rows is of another gate row, a part is a row
   int spread;        // 1: fewer rows than workers, workers counted across the CTAs
 };
 
 constexpr int kBwdOneCta = 16;    // up to so many rows one CTA does everything, in one launch
 constexpr int kBwdFewGroups = 64;  // a CTA column sums each gate row; beyond, a warp
-constexpr int kBwdUnit = 32;       // gate rows up to this length may be dealt whole
+// Gate rows that may be dealt whole: up to 32 rows, or 16 KB of each tensor.
+// 1M x 32 with 33 rows each takes 106 us dealt whole and 172 in shared parts,
+// 1M x 64 with 100 rows 221 and 318, 300k x 128 with 48 rows 126 and 183;
+// 300k x 256 with 100 rows (51 KB) 252 and 222.  Half as many gate rows as
+// workers are enough, as shared parts cost more than idle workers: at 0.55 of
+// them 0.58 to 0.91 of the time from 2 x 16 to 32 x 1024, at 0.4 of them 0.59
+// to 1.22.  With a CTA per row parts are few, and all of them are asked for.
+constexpr int kBwdUnit = 32, kBwdUnitElements = 8192;
 constexpr int kBwdThreads[4] = {512, 384, 256, 256};
 constexpr int kBwdCtaVpt[2] = {2, 4}, kBwdCtaWarps[2] = {16, 8};  // what the registers allow
 
@@ -403,7 +413,8 @@ NormBwdSplit norm_bwd_split(int M, int d, int rows) {
   s.ctas = std::min(total / per_cta, M);
   s.spread = M <= total ? 1 : 0;
   s.unit = 1;
-  const bool whole = s.rpg == 1 || (s.rpg <= kBwdUnit && s.groups >= total);
+  const bool short_rows = s.rpg <= kBwdUnit || static_cast<long long>(s.rpg) * d <= kBwdUnitElements;
+  const bool whole = s.rpg == 1 || (short_rows && (sh.cta ? 1LL : 2LL) * s.groups >= total);
   if (s.groups == 1) {
     s.team = total;
     s.run = M;
@@ -425,7 +436,15 @@ NormBwdSplit norm_bwd_split(int M, int d, int rows) {
       if (s.run - 1 <= s.rpg || s.team == per_cta) break;
     }
   }
-  s.slots = s.groups > 1 && !whole ? (s.run < 2 ? 1 : (s.run - 2) / s.rpg + 2) : 0;
+  // A worker's rows are a team apart: where that is a gate row or more, no two
+  // of them share one, and a part per row takes less than one per gate row of
+  // the run (138 MB at 65536 x 32 with 8 rows each, 9.7 so; 84 us, 18).  With a
+  // warp per row teams are small, and the place's arithmetic would spill.
+  s.by_row = s.groups > 1 && !whole && s.team >= s.rpg && sh.lpr < 32;
+  s.slots = s.groups == 1 || whole ? 0
+            : s.by_row             ? (s.run + s.team - 1) / s.team
+            : s.run < 2            ? 1
+                                   : (s.run - 2) / s.rpg + 2;
   return s;
 }
 
@@ -567,15 +586,21 @@ __global__ void __launch_bounds__(CTA ? 256 : kBwdThreads[VPT - 1], CTA && VPT =
     if (!one) spost[(2 * j) * nthr] = spost[(2 * j + 1) * nthr] = zero;
   }
   double salpha = 0.0;
-  const int g_first = by_rpg(r0 < p.M ? static_cast<int>(r0) : 0);
+  // what a gate row's place among the worker's parts is counted from
+  const int first = LPR < 32 && sp.by_row ? m0 : by_rpg(r0 < p.M ? static_cast<int>(r0) : 0);
   int g = -1;      // gate row of T
   int g_end = m0;  // where it ends
   // T of gate row g to its place, and its share of dw_post
   auto flush = [&]() {
     float* dst = nullptr;
+    int part = g - first;
+    if constexpr (LPR < 32) {
+      // by row, the worker's only row of gate row g is its first one from g * rpg on
+      if (sp.by_row) part = (g * sp.rpg - first + sp.team - 1) / sp.team;
+    }
     if (p.dgate != nullptr)
       dst = sp.slots == 0 ? p.dgate + static_cast<size_t>(g) * p.d
-                          : ws.gate + (static_cast<size_t>(me) * sp.slots + (g - g_first)) * p.d;
+                          : ws.gate + (static_cast<size_t>(me) * sp.slots + part) * p.d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       uint64_t w[4], o[4], f[4];
@@ -780,6 +805,15 @@ __device__ __forceinline__ float2 gate_parts(const NormGateBwd& p, const NormBwd
                                              int k0, int kn) {
   const uint32_t run = sp.run, team = sp.team, rpg = sp.rpg;
   const uint32_t r0 = g * rpg, r1 = min(r0 + rpg, static_cast<uint32_t>(p.M));
+  if (sp.by_row) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (uint32_t row = r0 + k0; row < r1; row += kn) {
+      const uint32_t t = row / run, i = row - t * run, slot = i / team;
+      add2(s, gate + (static_cast<size_t>(t * team + i - slot * team) * sp.slots + slot) * p.d + c);
+    }
+    return s;
+  }
   const uint32_t t0 = r0 / run, parts = ((r1 - 1) / run - t0 + 1) * team;
   float2 s = make_float2(0.f, 0.f);
 #pragma unroll 4

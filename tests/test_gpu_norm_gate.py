@@ -329,3 +329,18 @@ def test_offsets_beyond_32_bits():
     s = dict(rn=want["r_next"], rpost=want["rstd_post"], rpre=want["rstd_pre"], dx=want["x"], drn=None)
     got = bwd(sub, s, 50, d, 50, drn=False)
     assert torch.equal(dr[-50:], got["dr"]) and torch.equal(dy[-50:], got["dy"])
+
+
+@pytest.mark.parametrize("M,d,rows", [
+    # parts by row: a worker's rows are of different gate rows; the last gate row and the last run are short
+    (20011, 16, 100), (9001, 32, 60), (5003, 64, 33), (2500, 128, 30), (30011, 16, 128), (65539, 32, 8), (19000, 16, 2),
+    (4737, 128, 32), (9473, 64, 64),
+    # fewer gate rows than workers, dealt whole; narrow gate rows of more than 32 rows, dealt whole
+    (20001, 768, 30), (2500, 768, 4), (1301, 256, 1), (2601, 208, 2), (1200 * 33 + 7, 256, 32), (5000 * 50 + 11, 128, 50),
+    (9500 * 60 + 1, 16, 60)])
+def test_gradient_of_short_gate_rows(M, d, rows):
+    p = inputs(M, d, rows, seed=M + d)
+    s = saved(p, M, d, rows)
+    check(bwd(p, s, M, d, rows), p, s, M, rows)
+    skip = bwd(p, s, M, d, rows, skip=("dw_post", "dalpha", "dw_pre"))
+    assert torch.equal(skip["dgate"], bwd(p, s, M, d, rows)["dgate"])

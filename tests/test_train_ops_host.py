@@ -2,6 +2,8 @@
 optimizer (no GPU needed: arguments are checked before any CUDA call), the
 descriptor's layout, and the plain definitions against differences."""
 import ctypes
+import math
+import random
 import re
 
 import pytest
@@ -381,3 +383,16 @@ def test_gradient_norm_refuses_overlaps():
     if not torch.cuda.is_available():
         refused(A.ERR_NO_DEVICE, A.fp8mlp_grad_norm, arr, 1.0, out, ws)
         refused(A.ERR_NO_DEVICE, A.fp8mlp_grad_norm, arr, 1.0, (1 << 24) + 400, (1 << 20) - 48)
+
+
+def test_norm_workspace_stays_small():
+    # parts of gate rows: at most two to three times a tensor of the call, and what 148 SMs' workers take at least
+    rng = random.Random(5)
+    log = lambda lo, hi: int(math.exp(rng.uniform(math.log(lo), math.log(hi))))  # noqa: E731
+    cases = [(65536, 32, 8), (16384, 64, 8), (1000000, 64, 33), (72600000, 16, 33), (16384, 64, 9472), (20005, 16, 2)]
+    for _ in range(20000):
+        M, d = log(1, 5e6), 16 * log(1, 512)
+        cases.append((M, d, log(1, M + 1)))
+    for M, d, rows in cases:
+        need = A.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows)
+        assert need <= 2.5 * (2 * M * d) + (16 << 20), (M, d, rows, need)
