@@ -57,6 +57,7 @@ cudaError_t launch_block_gemm(bool relu2, bool pairs, BlockGemmParams& p, int nu
 // the product for few rows; x: bf16, quantised on the way (xq and xs are
 // written), or NULL: xq and xs are read
 constexpr int kGemvMaxM = 8, kGemvMaxUp = 4;
+// whether it is the faster form
 bool block_gemv_fits(bool relu2, int M, int K, int N);
 cudaError_t launch_block_gemv(int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,
                               const float* ws, uint16_t* y, int num_sms, cudaStream_t s);

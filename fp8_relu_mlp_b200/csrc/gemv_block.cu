@@ -10,6 +10,7 @@
 // in fp32; a lane's sixteen belong to one scale block, so the factor
 // xs * ws is applied once per sixteen.
 #include <atomic>
+#include <cmath>
 
 #include "block.h"
 
@@ -295,16 +296,32 @@ cudaError_t launch_m(int K, int N, const uint16_t* x, uint8_t* xq, float* xs, co
 
 }  // namespace
 
-// The pass over the weights costs 2.2 us and 0.15 ns per thousand
-// multiply-adds, the tensor cores (with the quantiser) 4.6 us and 0.42 us per
-// 128 of K and wave of 148 tiles: 3 against 7 us at 4 x 768 -> 2304, 10 against
-// 11 at 8 x 2048 -> 2048, 48 against 18 at 8 x 768 -> 50304.
-// The up-projection's clusters start a microsecond later and its tensor-core
-// form takes 5.8 us (and 2 us for the quantiser) at 1024 -> 4096: 4.9 us at one
-// row, 6.1 at four, 9.1 at eight.
+// Estimated times of both forms in ns, fitted to 310 measured shapes (M 1 to 8,
+// K 16 to 4096, N 16 to 50304, weights from HBM) and checked on 400 others.  The
+// pass over the weights: a start, groups of 128 quantised or unpacked 16 at a
+// time by every CTA, and per column the sums over lanes (by M) and loads of 512
+// codes (by K); the up-projection's start has its clusters'.  The tensor cores: a
+// start, a k-block after the other, and the weights' way.  Calls from BF16 rows,
+// whose quantiser the pass takes along, and from codes take the same form, so
+// that they give the same bits: the starts are the mean of both.  The choice
+// takes 1 to 3 % more than the faster form on average and half as much again
+// at most.  Us from BF16 rows: 1 x 768 -> 2304 2.6 by the pass and 5.8 by the
+// tensor cores, 8 x 768 -> 4096 7.5 and 6.1, 8 x 512 -> 16384 15.3 and 8.5, 1 x 4096
+// -> 50304 53 and 69; up-projection from codes 1 x 1024 -> 4096 5.8 and 6.1,
+// 4 x 1024 -> 4096 6.4 and 6.1.
 bool block_gemv_fits(bool relu2, int M, int K, int N) {
-  return M <= (relu2 ? kGemvMaxUp : kGemvMaxM) && gemv_smem(M, K) <= static_cast<size_t>(kSmemMost) &&
-         static_cast<long long>(M) * K * N <= (1ll << 26);
+  if (M > (relu2 ? kGemvMaxUp : kGemvMaxM) || gemv_smem(M, K) > static_cast<size_t>(kSmemMost)) return false;
+  const float kb = static_cast<float>((K + kBlock - 1) / kBlock), loads = static_cast<float>((K + 511) / 512);
+  const float rounds = ceilf(M * kb / 16), m = static_cast<float>(M), n = static_cast<float>(N) * 1e-3f;
+  float pass, tensor;
+  if (relu2) {
+    pass = 2325.f + 1250.f * rounds + n * (35.f + 65.f * m + loads * (150.f + 5.f * m));
+    tensor = 3500.f + 260.f * kb + n * (120.f + 32.f * kb);
+  } else {
+    pass = 1125.f + 740.f * rounds + 85.f * m + n * (45.f * m + loads * (105.f + 20.f * m));
+    tensor = 2900.f + 260.f * kb + n * (100.f + 26.f * kb);
+  }
+  return pass < tensor;
 }
 
 cudaError_t launch_block_gemv(int M, int K, int N, const uint16_t* x, uint8_t* xq, float* xs, const uint8_t* Wq,

@@ -353,3 +353,24 @@ def test_the_mlp_may_write_over_its_input(M):
         sq = torch.zeros(M, d, dtype=BF, device="cuda")
         A.fp8mlp_linear_block(M, d, d, sq, W1q[:d].contiguous(), w1s, torch.empty(M, d, dtype=U8, device="cuda"),
                               torch.empty(2, M, device="cuda"), sq)
+
+
+@pytest.mark.parametrize("M,K,N,one", [(1, 768, 2304, True), (1, 4096, 50304, True), (1, 16, 16, True), (4, 2048, 1024, True),
+                                       (8, 512, 16384, False), (8, 128, 50304, False), (6, 768, 8192, False),
+                                       (2, 16, 50304, False), (9, 64, 64, False)])
+def test_few_rows_take_the_faster_form(M, K, N, one):
+    # one launch where the pass over the weights is faster, two where the tensor cores are
+    x = randn(M, M, K)
+    Wq = torch.randint(0, 0x70, (N, K), dtype=U8, device="cuda", generator=gen(1))
+    ws = torch.rand(R.cdiv(K, 128), R.cdiv(N, 128), device="cuda", generator=gen(2)) * 1e-2
+    xq, xs, y = torch.empty(M, K, dtype=U8, device="cuda"), torch.empty(R.cdiv(K, 128), M, device="cuda"), torch.empty(M, N, dtype=BF, device="cuda")
+    n0 = A.fp8mlp_kernel_launch_count()
+    A.fp8mlp_linear_block(M, K, N, x, Wq, ws, xq, xs, y)
+    assert A.fp8mlp_kernel_launch_count() - n0 == (1 if one else 2)
+    # from codes the same form, bit for bit
+    again = torch.empty_like(y)
+    A.fp8mlp_linear_fwd_block(M, K, N, xq, xs, Wq, ws, again)
+    torch.cuda.synchronize()
+    assert torch.equal(y, again) and A.fp8mlp_get_device_status() == 0
+    exact, mag = R.product(xq.view(torch.float8_e4m3fn), xs, Wq.view(torch.float8_e4m3fn), ws)
+    assert within(y, exact, mag, K + 2 * R.cdiv(K, 128) + 4)
