@@ -374,3 +374,16 @@ def test_few_rows_take_the_faster_form(M, K, N, one):
     assert torch.equal(y, again) and A.fp8mlp_get_device_status() == 0
     exact, mag = R.product(xq.view(torch.float8_e4m3fn), xs, Wq.view(torch.float8_e4m3fn), ws)
     assert within(y, exact, mag, K + 2 * R.cdiv(K, 128) + 4)
+
+
+def test_the_whole_mlp_repeats_itself():
+    M, d, h = 2000, 1024, 4096
+    x, W1, W2 = randn(M, M, d), randn(2, h, d, scale=d ** -0.5), randn(3, h, d, scale=h ** -0.5)
+    W1q, w1s, _, _ = weight(W1)
+    _, _, W2qt, w2st = weight(W2)
+    first = None
+    for i in range(8):
+        o = [torch.full(s, 0x55, dtype=U8, device="cuda") for s in ((M, d), (M, 32), (M, 2 * h), (M, h), (M, 128), (M, 2 * d))]
+        A.fp8mlp_mlp_fwd_block(M, d, h, x, W1q, w1s, W2qt, w2st, o[0], o[1], o[2], o[3], o[4], o[5])
+        first = first or o
+        assert all(torch.equal(a, b) for a, b in zip(first, o))
