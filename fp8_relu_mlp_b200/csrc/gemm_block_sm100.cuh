@@ -14,7 +14,7 @@
 //   warp 0      TMA producer: A/B k-blocks into a STAGES-deep ring
 //   warp 1      allocates TMEM, issues the UMMAs from one thread
 //   warp 2      pairs: stores finished tiles (TMA)
-//   next        scales of each stage to shared memory
+//   next        scales of each k-block to shared memory
 //   then        4 * BN / 128 epilogue warps
 // What bounds it: a k-block of a 256 x 256 tile is 512 cycles of tensor work;
 // issuing it takes 500 to 560, and its promotion (128 columns of TMEM and 128
@@ -88,14 +88,23 @@ struct BlockCfg {
   // output: chunks of 128 rows x 128 bytes, 64 columns of bf16 or 128 codes
   static constexpr int CHUNK = BM * 128;
   static constexpr int OUT_CHUNKS = BN / 64 + (RELU2 ? BN / 128 : 0);
-  // ring of scales: a k-block's are 128 rows' and BN / 128 weight blocks'.  A
-  // slot is free once the UMMAs NBUF k-blocks behind its last use are done
-  // (they waited for that use's accumulator); the wait for those must not see
-  // the barrier's next phase, which holds for SRING <= NBUF + STAGES.
+  // ring of scales: a k-block's are 128 rows' and BN / 128 weight blocks'.
+  // A single CTA announces them with its loads: the UMMAs wait for both, and
+  // their completion tells the epilogue.  A slot is free once the UMMAs NBUF
+  // k-blocks behind its last use are done (they waited for that use's
+  // accumulator); the wait for those must not see the barrier's next phase,
+  // which holds for SRING <= NBUF + STAGES.
+  // A pair's UMMAs are issued by one CTA: that way would pass signals between
+  // CTAs, which order the other's own shared memory only with a release at
+  // cluster scope (1000 cycles behind the loads under way).  So each CTA of a
+  // pair has barriers of its own for the slots (the up-projection takes 1 to 2 %
+  // longer for it, the plain product no longer); a single CTA with few tiles
+  // would lose 5 to 20 %.
   static constexpr int SCALES = 132 * 4;
   static constexpr int SRING = NBUF == 2 ? 4 : 8;
-  static_assert(SRING > NBUF && SRING <= NBUF + STAGES && SRING - NBUF <= STAGES, "scale ring");
-  static constexpr int NUM_BARS = 2 * STAGES + NBUF + 3;
+  static constexpr bool SLOT_BARS = CG == 2;
+  static_assert(SLOT_BARS || (SRING > NBUF && SRING <= NBUF + STAGES && SRING - NBUF <= STAGES), "scale ring");
+  static constexpr int NUM_BARS = 2 * STAGES + NBUF + (SLOT_BARS ? 2 * SRING : 0) + 3;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SRING * SCALES + OUT_CHUNKS * CHUNK + NUM_BARS * 8 + 16;
   static_assert(CG == 1 || CG == 2, "CTA group");
   static_assert(BN == 128 || BN == 256, "accumulators");
@@ -123,12 +132,6 @@ __device__ __forceinline__ float ld_scale(const float* p, bool valid) {
       : "=f"(v)
       : "l"(p), "r"(static_cast<int>(valid)));
   return v;
-}
-
-// arrive on an mbarrier of another CTA of the pair, after this warp's stores to
-// its own shared memory (read by its own CTA only)
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // one lane of a converged warp
@@ -196,8 +199,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
   uint64_t* full = reinterpret_cast<uint64_t*>(sScale + C::SRING * (C::SCALES / 4));
   uint64_t* done = full + C::STAGES;
   uint64_t* tempty = done + C::STAGES;
-  uint64_t* oready = tempty + C::NBUF;  // a tile's output is in shared memory
-  uint64_t* ofree = oready + 1;         // it has been read from there
+  uint64_t* sfull = tempty + C::NBUF;    // SLOT_BARS: a slot's scales are there,
+  uint64_t* sempty = sfull + C::SRING;   // and have been read
+  uint64_t* oready = sfull + (C::SLOT_BARS ? 2 * C::SRING : 0);  // a tile's output is in shared memory
+  uint64_t* ofree = oready + 1;          // it has been read from there
   uint64_t* fin = ofree + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -211,11 +216,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1 + CG);  // the loads, and each CTA's scales
+      mbar_init(&full[s], C::SLOT_BARS ? 1 : 2);  // the loads, and the scales
       mbar_init(&done[s], 1);
     }
     for (int a = 0; a < C::NBUF; ++a) {
       mbar_init(&tempty[a], C::NEPI * CG);  // one arrival per epilogue warp of the pair
+    }
+    for (int i = 0; C::SLOT_BARS && i < C::SRING; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], C::NEPI);
     }
     mbar_init(oready, C::NEPI);
     mbar_init(ofree, 1);
@@ -392,47 +401,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
       float v[4][5];
 #pragma unroll
       for (int j = 0; j < 4; ++j) load(v[j]);
-      const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
-      // from here on a slot, or its stage's barrier, is not in its first round
-      constexpr int kFirst = C::SRING < C::STAGES ? C::SRING : C::STAGES;
       const long long my_tiles = unit < num_tiles ? (num_tiles - unit + nunits - 1) / nunits : 0;
       const long long steps = my_tiles * num_kb;
-      uint32_t stage = 0, slot = 0, wstage = kFirst - C::SRING + C::NBUF, wphase = 0;
+      // from here on a slot, or its stage's barrier, is not in its first round
+      constexpr int kFirst = C::SRING < C::STAGES ? C::SRING : C::STAGES;
+      uint32_t stage = 0, slot = 0, sphase = 1, wstage = kFirst - C::SRING + C::NBUF, wphase = 0;
       bool ok = true;
       for (long long g0 = 0; g0 < steps && ok; g0 += 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (g0 + j >= steps) break;
-          if (g0 + j >= kFirst) {
-            if (!mbar_wait_inline(&done[wstage], wphase, w)) {
-              ok = false;
-              break;
-            }
+          if constexpr (C::SLOT_BARS) {
+            ok = mbar_wait_inline(&sempty[slot], sphase, w);
+          } else if (g0 + j >= kFirst) {
+            ok = mbar_wait_inline(&done[wstage], wphase, w);
             if (++wstage == C::STAGES) {
               wstage = 0;
               wphase ^= 1u;
             }
           }
+          if (!ok) break;
           float* s = sScale + slot * (C::SCALES / 4);
-          if (++slot == C::SRING) slot = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[lane + i * 32] = v[j][i];
           if (lane < C::BN / 128) s[128 + lane] = v[j][4];
           __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 1)
-              mbar_arrive(&full[stage]);
-            else
-              mbar_arrive_remote(full0 + stage * 8u);
-          }
+          if (lane == 0) mbar_arrive(C::SLOT_BARS ? &sfull[slot] : &full[stage]);
           load(v[j]);
+          if (++slot == C::SRING) {
+            slot = 0;
+            sphase ^= 1u;
+          }
           if (++stage == C::STAGES) stage = 0;
         }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // (scales: in place before the UMMAs of their stage were issued)
     if constexpr (C::SPLIT_REGS) reg_inc<C::REGS_EPI>();
     const int q = warp & 3;  // TMEM lane quarter
     const int e = warp - C::EPI0;
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
     const uint32_t orow = smem_u32(sOut) + (e >> 2) * (2 * C::CHUNK) + (q * 32 + lane) * 128;  // this thread's row, bf16
     const uint32_t qrow = smem_u32(sOut) + (C::BN / 64 + (e >> 2)) * C::CHUNK + (q * 32 + lane) * 128;  // codes
     const uint32_t xor16 = (lane & 7) << 4;  // of the 128-byte swizzle
-    uint32_t buf = 0, stage = 0, phase = 0, slot = 0, ofree_phase = 1;
+    uint32_t buf = 0, stage = 0, phase = 0, slot = 0, sphase = 0, ofree_phase = 1;
 
     // this warp's rows of a chunk, out
     auto store_part = [&](const CUtensorMap* map, int chunk, int col, int row) {
@@ -462,6 +467,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
+        float f = 0.f;
+        auto factor = [&]() {
+          const float* sc = sScale + slot * (C::SCALES / 4);
+          f = __fmul_rn(sc[q * 32 + lane], sc[128 + (c0 >> 7)]);
+        };
+        if constexpr (C::SLOT_BARS) {
+          if (!mbar_wait_inline(&sfull[slot], sphase, w)) {
+            ok = false;
+            break;
+          }
+          factor();
+        }
         if (!mbar_wait_inline(&done[stage], phase, w)) {
           ok = false;
           break;
@@ -471,9 +488,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
         uint32_t v[2][16];
         const uint32_t src = tmem_mine + buf * C::BN;
         tmem_ld16_issue(src, v[0]);
-        const float* sc = sScale + slot * (C::SCALES / 4);
-        if (++slot == C::SRING) slot = 0;
-        const float f = __fmul_rn(sc[q * 32 + lane], sc[128 + (c0 >> 7)]);
+        if constexpr (!C::SLOT_BARS) factor();
         const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -488,6 +503,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
                 mbar_arrive(&tempty[buf]);
               else
                 mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
+              if constexpr (C::SLOT_BARS) mbar_arrive(&sempty[slot]);
             }
           }
 #pragma unroll
@@ -496,6 +512,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gemm_block_kernel(const __grid_
                 f2_pack(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), f2, acc[c * 8 + i]);
         }
         if (++buf == C::NBUF) buf = 0;
+        if (++slot == C::SRING) {
+          slot = 0;
+          sphase ^= 1u;
+        }
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
