@@ -974,8 +974,13 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
 namespace {
 
 // ---- block-scaled FP8 products ----------------------------------------------
+constexpr int kMaxRows = 0x7FFFF000;  // a row index rounded up to a tile, or a worker's next row, stays an int
+int check_rows(int M) {
+  return M <= kMaxRows ? FP8MLP_OK : fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "M must be <= 2^31 - 4096");
+}
 int check_block_dims(int M, int a, int b) {
   TRY(check_dims(M, a, b));
+  TRY(check_rows(M));
   if (a > (1 << 22) || b > (1 << 22)) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "widths must be <= 2^22");
   return FP8MLP_OK;
 }
@@ -1310,6 +1315,7 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
                          fp8mlp_stream_t stream) {
   g_detail.clear();
   TRY(check_dims(M, d, 16));
+  TRY(check_rows(M));
   if (d > kNormMaxD) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "d must be <= 8192");
   if (!(eps > 0.f) || !std::isfinite(eps)) return fail(FP8MLP_ERR_INVALID_ARG, "eps must be finite and > 0");
   if (rows_per_gate < 1) return fail(FP8MLP_ERR_INVALID_ARG, "rows_per_gate < 1");
@@ -1360,7 +1366,7 @@ int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, con
 }
 
 size_t fp8mlp_norm_gate_bwd_workspace_size(int M, int d, int rows_per_gate) {
-  if (M <= 0 || d <= 0 || d > kNormMaxD || rows_per_gate <= 0) return 0;
+  if (M <= 0 || M > kMaxRows || d <= 0 || d > kNormMaxD || rows_per_gate <= 0) return 0;
   return norm_gate_bwd_workspace(M, d, rows_per_gate);
 }
 
@@ -1371,6 +1377,7 @@ int fp8mlp_norm_gate_bwd(int M, int d, const uint16_t* r, const uint16_t* y, con
                          float* dalpha, float* dw_pre, void* workspace, fp8mlp_stream_t stream) {
   g_detail.clear();
   TRY(check_dims(M, d, 16));
+  TRY(check_rows(M));
   if (d > kNormMaxD) return fail(FP8MLP_ERR_UNSUPPORTED_SHAPE, "d must be <= 8192");
   if (rows_per_gate < 1) return fail(FP8MLP_ERR_INVALID_ARG, "rows_per_gate < 1");
   if (dw_post != nullptr) REQUIRE_PTR(dw_post);

@@ -405,7 +405,7 @@ NormShape norm_bwd_shape(int d, int groups, int tensors) {
 NormBwdSplit norm_bwd_split(int M, int d, int rows) {
   NormBwdSplit s = {};
   s.rpg = rows < M ? rows : M;
-  s.groups = (M + s.rpg - 1) / s.rpg;
+  s.groups = (M - 1) / s.rpg + 1;
   const NormShape sh = norm_bwd_shape(d, s.groups, 5);
   const int per_cta = sh.cta ? 1 : sh.threads / sh.lpr;
   int total = kSms * sh.per_sm * per_cta;
@@ -432,7 +432,7 @@ NormBwdSplit norm_bwd_split(int M, int d, int rows) {
     for (s.team = per_cta * (sh.cta ? 16 : 8);; s.team /= 2) {
       if (total % s.team != 0) continue;
       const int teams = total / s.team;
-      s.run = (M + teams - 1) / teams;
+      s.run = (M - 1) / teams + 1;
       if (s.run - 1 <= s.rpg || s.team == per_cta) break;
     }
   }

@@ -487,7 +487,7 @@ int fp8mlp_residual_add(int M, int d, const uint16_t* r, const uint16_t* out, ui
  * is computed from it is NaN.  Scales are fp32, block of the contraction
  * outermost: xs [ceil(K/128)][M], ws [ceil(K/128)][ceil(N/128)].  The last
  * group and the last weight blocks may be shorter.  4-byte alignment is
- * enough for the scales.  Widths (K, N, d, h) <= 2^22.
+ * enough for the scales.  Widths (K, N, d, h) <= 2^22, M <= 2^31 - 4096.
  *   y[m,n] = bf16( sum_b fp32(xs[b,m] ws[b,n/128]) sum_{k in b} xq[m,k] Wq[n,k] )
  * with fp32 sums.  The gradient with respect to x is the same product over
  * the transposed cache, fp8mlp_linear_block(M, N, K, dY, Wq_t, ws_t, ...);
@@ -547,7 +547,7 @@ int fp8mlp_mlp_fwd_block(int M, int d, int h, const uint16_t* x, const uint8_t* 
  * and xs are NULL); not both.  xq, xs (both or neither): x quantised
  * as by fp8mlp_quantize_block, rounded once from fp32.  r_next may equal r, x may
  * equal y; no other output may overlap an array of the call
- * (FP8MLP_ERR_INVALID_ARG).  d <= 8192.  eps finite and > 0.
+ * (FP8MLP_ERR_INVALID_ARG).  d <= 8192, M <= 2^31 - 4096.  eps finite and > 0.
  * ------------------------------------------------------------------------ */
 int fp8mlp_norm_gate_fwd(int M, int d, const uint16_t* r, const uint16_t* y, const uint16_t* w_post,
                          const uint16_t* gate, int rows_per_gate, const float* alpha, const uint16_t* w_pre, float eps,

@@ -396,3 +396,25 @@ def test_norm_workspace_stays_small():
     for M, d, rows in cases:
         need = A.fp8mlp_norm_gate_bwd_workspace_size(M, d, rows)
         assert need <= 2.5 * (2 * M * d) + (16 << 20), (M, d, rows, need)
+
+
+@pytest.mark.parametrize("M", [2 ** 31 - 4095, 2 ** 31 - 256, 2 ** 31 - 1])
+def test_rows_next_to_2_31_are_refused(M):
+    for name, (fn, sizes, ptrs) in BLOCK_CALLS.items():
+        refused(SHAPE, fn, M, *[16] * (len(sizes) - 1), *ptrs)
+    refused(SHAPE, A.fp8mlp_norm_gate_fwd, *dict(FWD, M=M, d=16, rows_per_gate=M).values())
+    refused(SHAPE, A.fp8mlp_norm_gate_bwd, *dict(BWD, M=M, d=16, rows_per_gate=M).values())
+    assert A.fp8mlp_norm_gate_bwd_workspace_size(M, 16, M) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 2, 33, 1000, 2 ** 30, 2 ** 31 - 4097, 2 ** 31 - 4096, 2 ** 31 - 1])
+def test_the_most_rows(rows):
+    M = 2 ** 31 - 4096
+    need = A.fp8mlp_norm_gate_bwd_workspace_size(M, 16, rows)
+    assert 0 < need <= 4.5 * M * 16  # a part per row at most, and a bit
+    if not torch.cuda.is_available():
+        far = lambda d: dict(d, **{k: (i + 1) << 44 for i, k in enumerate(k for k, v in d.items() if v == F)})  # noqa: E731
+        refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_bwd, *dict(far(BWD), M=M, d=16, rows_per_gate=rows).values())
+        refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_fwd, *dict(far(FWD), M=M, d=16, rows_per_gate=rows).values())
+        for name, (fn, sizes, ptrs) in BLOCK_CALLS.items():
+            refused(A.ERR_NO_DEVICE, fn, M, *[16] * (len(sizes) - 1), *[(i + 1) << 44 for i in range(len(ptrs))])
