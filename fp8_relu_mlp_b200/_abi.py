@@ -574,7 +574,7 @@ class AdamwTensor(ctypes.Structure):
 def adamw_tensor(n, p, p_bf16, g, m, v, m_scale=None, v_scale=None, lr_mult=1.0, weight_decay=0.0, state_bits=32):
     """One descriptor for :func:`fp8mlp_adamw_step`, its tensors' sizes checked.
     It holds addresses: the tensors have to stay alive."""
-    dev = _here(0)[0]
+    dev = (_current or _no_gpu)()[0]
     sb, nb = state_bits // 8, 4 * _kblocks(n)
     return AdamwTensor(n, _buf(p, 4 * n, "p", dev), _buf(p_bf16, 2 * n, "p_bf16", dev), _buf(g, 4 * n, "g", dev),
                        _buf(m, sb * n, "m", dev), _buf(v, sb * n, "v", dev), _buf(m_scale, nb, "m_scale", dev),

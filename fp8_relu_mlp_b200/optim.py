@@ -12,7 +12,7 @@ device.
 from __future__ import annotations
 
 import math
-from bisect import bisect, insort
+from bisect import bisect
 
 import torch
 
@@ -41,7 +41,7 @@ class AdamW:
         self._descriptors = []
         self._plan = self._workspace = None
         self._outgrown = []  # workspaces that steps under way or captured ones may still use
-        self._extents = []  # first and last address of every tensor, in order
+        self._first, self._behind = [], []  # addresses of every tensor's first byte, in order, and behind its last
         self.state = torch.empty(8, dtype=torch.int32, device=self.device)  # fp8mlp_adamw_state (32 bytes)
         self.norm = torch.zeros(2, dtype=torch.float32, device=self.device)  # gradient norm, clip coefficient
         self._coef = self.norm[1:]
@@ -78,18 +78,30 @@ class AdamW:
             if state["m_scale"].dtype != torch.float32 or state["v_scale"].dtype != torch.float32:
                 raise ValueError("m_scale and v_scale must be fp32")
         e = dict(grad=grad, master=master, weight=weight, **state)
-        given = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in e.values() if t is not None and t.numel())
-        known = self._extents
-        for k, x in enumerate(given):
-            i = bisect(known, x)
-            if ((k > 0 and given[k - 1][1] > x[0]) or (i > 0 and known[i - 1][1] > x[0]) or
-                    (i < len(known) and known[i][0] < x[1])):
-                raise ValueError("a tensor is given twice, or overlaps another: one step updates each weight once")
-        self._descriptors.append(A.adamw_tensor(
-            n, master, weight, grad, state["m"], state["v"], state.get("m_scale"), state.get("v_scale"), lr_mult,
-            weight_decay, self.state_bits))
-        for x in given:
-            insort(known, x)
+        firsts, behinds = self._first, self._behind
+        added = []  # this parameter's, taken back where it is refused
+        try:
+            for t in e.values():
+                if t is None:
+                    continue
+                first = t.data_ptr()
+                behind = first + t.nbytes
+                if first == behind:
+                    continue
+                i = bisect(firsts, first)
+                if (i and behinds[i - 1] > first) or (i < len(firsts) and firsts[i] < behind):
+                    raise ValueError("a tensor is given twice, or overlaps another: one step updates each weight once")
+                firsts.insert(i, first)
+                behinds.insert(i, behind)
+                added.append(first)
+            self._descriptors.append(A.adamw_tensor(
+                n, master, weight, grad, state["m"], state["v"], state.get("m_scale"), state.get("v_scale"), lr_mult,
+                weight_decay, self.state_bits))
+        except Exception:
+            for first in added:
+                i = bisect(firsts, first) - 1
+                del firsts[i], behinds[i]
+            raise
         self.entries.append(e)
         self._plan = None
         return e
