@@ -576,14 +576,18 @@ def adamw_tensor(n, p, p_bf16, g, m, v, m_scale=None, v_scale=None, lr_mult=1.0,
     It holds addresses: the tensors have to stay alive."""
     dev = (_current or _no_gpu)()[0]
     sb, nb = state_bits // 8, 4 * _kblocks(n)
-    return AdamwTensor(n, _buf(p, 4 * n, "p", dev), _buf(p_bf16, 2 * n, "p_bf16", dev), _buf(g, 4 * n, "g", dev),
-                       _buf(m, sb * n, "m", dev), _buf(v, sb * n, "v", dev), _buf(m_scale, nb, "m_scale", dev),
-                       _buf(v_scale, nb, "v_scale", dev), lr_mult, weight_decay)
+    t = AdamwTensor(n, _buf(p, 4 * n, "p", dev), _buf(p_bf16, 2 * n, "p_bf16", dev), _buf(g, 4 * n, "g", dev),
+                    _buf(m, sb * n, "m", dev), _buf(v, sb * n, "v", dev), _buf(m_scale, nb, "m_scale", dev),
+                    _buf(v_scale, nb, "v_scale", dev), lr_mult, weight_decay)
+    t.state_bits = state_bits
+    return t
 
 
 def adamw_tensors(descriptors):
     """The array the calls below take; build it once, use it every step."""
-    return (AdamwTensor * len(descriptors))(*descriptors)
+    arr = (AdamwTensor * len(descriptors))(*descriptors)
+    arr.state_bits = {t.state_bits for t in descriptors if t.m and hasattr(t, "state_bits")}  # that their sizes were held to
+    return arr
 
 
 def _tensors(arr):
@@ -616,6 +620,9 @@ def fp8mlp_adamw_check(tensors, st, state_bits, grad_coef=None):
 
 
 def fp8mlp_adamw_step(tensors, st, state_bits, beta1, beta2, eps, grad_coef=None, stream=None):
+    for bits in getattr(tensors, "state_bits", ()):
+        if bits != state_bits:
+            raise ValueError(f"the descriptors were made for {bits}-bit states, not {state_bits}")
     if _marshal is not None:
         return _done(_marshal.adamw_step(*_tensors(tensors), st, state_bits, beta1, beta2, eps, grad_coef, stream),
                      "fp8mlp_adamw_step")

@@ -23,7 +23,8 @@ from ._order import after_current, as_stream, used_on
 class AdamW:
     """With a ``stream`` of its own, what the optimizer launches waits for the
     current stream's work so far; nothing waits for the optimizer but
-    ``set_lr`` and ``read_state``.  Parameters may be added between steps; a
+    ``set_lr`` and ``read_state``, and a capture is made on that stream.
+    Parameters may be added between steps; a
     step captured before goes on with the parameters that it had."""
 
     def __init__(self, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8, seed: int = 0,

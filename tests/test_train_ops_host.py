@@ -418,3 +418,17 @@ def test_the_most_rows(rows):
         refused(A.ERR_NO_DEVICE, A.fp8mlp_norm_gate_fwd, *dict(far(FWD), M=M, d=16, rows_per_gate=rows).values())
         for name, (fn, sizes, ptrs) in BLOCK_CALLS.items():
             refused(A.ERR_NO_DEVICE, fn, M, *[16] * (len(sizes) - 1), *[(i + 1) << 44 for i in range(len(ptrs))])
+
+
+def test_descriptors_of_other_state_bits_are_refused():
+    at = lambda i: (i + 1) << 24  # noqa: E731
+    made = {b: A.adamw_tensor(1000, at(0), None, at(1), at(2), at(3), at(4), at(5), state_bits=b) for b in (8, 32)}
+    for have, asked in ((8, 32), (32, 8)):
+        for ts in ([made[have]], [made[asked], made[have]]):
+            with pytest.raises(ValueError, match=f"{have}-bit"):
+                A.fp8mlp_adamw_step(A.adamw_tensors(ts), ST, asked, 0.9, 0.95, 1e-8, stream=0)
+    if not torch.cuda.is_available():
+        for b in (8, 32):
+            refused(A.ERR_NO_DEVICE, A.fp8mlp_adamw_step, A.adamw_tensors([made[b]]), ST, b, 0.9, 0.95, 1e-8, None)
+    # gradients alone, for the norm, have no states
+    A.adamw_tensors([A.adamw_tensor(10, None, None, at(0), None, None), made[8]])
