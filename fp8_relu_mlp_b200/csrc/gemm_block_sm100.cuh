@@ -18,16 +18,16 @@
 //   then        4 * BN / 128 epilogue warps
 // What bounds it: a k-block of a 256 x 256 tile is 512 cycles of tensor work;
 // issuing it takes 500 to 560, and its promotion (128 columns of TMEM and 128
-// multiply-adds per epilogue thread) some 600, with the hand-over of two
-// accumulators between them.  8192 x 4096 -> 1024 runs at 2.3 PFLOP/s (29.7 us;
-// an unscaled e4m3 library product of that size takes 24.4), 16384 x 768 ->
-// 2304, where writing y weighs as much as the six k-blocks, at 1.9 (30.5 us;
-// 29.0).  Steps that gained, in us of the latter: no release fence in the
-// hand-over and pipelined TMEM reads 80 to 41, 128-byte output rows 38, one
-// commit per k-block 37, a store thread 35, elected issue 34.5, scales by a warp
-// of their own 30.5.  Measured and not taken: 256 x 128 tiles (L2 and
-// hand-over bound, 50), 16 epilogue warps (47), output straight from registers
-// (44), A kept in shared memory along N (38).
+// multiply-adds per epilogue thread) some 600 (clock reads in a copy of the
+// kernel), with the hand-over of two accumulators between them.  Back to back,
+// 8192 x 4096 -> 1024 takes 30 to 31 us (2.2 PFLOP/s; an unscaled e4m3 library
+// product of that size 24.4), 16384 x 768 -> 2304, where writing y weighs as much
+// as the six k-blocks, 29.4 to 30 (2.0; 29.0).  Steps that gained, in us of the
+// latter as each was built: no release fence in the hand-over and pipelined TMEM
+// reads 80 to 41, 128-byte output rows 38, one commit per k-block 37, a store
+// thread 35, elected issue 34.5, scales by a warp of their own 30.5.  Measured and
+// not taken: 256 x 128 tiles (L2 and hand-over bound, 50), 16 epilogue warps (47),
+// output straight from registers (44), A kept in shared memory along N (38).
 // CG = 2: the CTAs of a cluster pair share a 2-CTA UMMA over 256 rows, as in
 // gemm_sm100.cuh.  TMA zero-fills rows and columns past the edges and clips
 // the stores.

@@ -10,11 +10,11 @@
 // a CTA.  Workers are persistent and copy their next rows to shared memory
 // while they compute the current one (cp.async, each thread its own 16-byte
 // vectors, so no barrier is needed): the two dependent reductions of a row
-// would otherwise leave HBM idle.  Measured at 16384 x 768: forward with the FP8
-// copy 19.5 us (5.8 TB/s, 0.89 of the copy rate; 24.1 without the ring),
-// gradient 37 us (4.7 TB/s: 730 instructions per row and warp with eight warps
-// per SM, which its registers allow, come next to HBM); 7777 x 2064 with a gate
-// per 1000 rows, a CTA per row, 66 us.
+// would otherwise leave HBM idle.  Measured back to back at 16384 x 768: forward
+// with the FP8 copy 19.5 us (5.8 TB/s, 0.89 of the copy rate; 24.1 without the
+// ring), gradient 38 us (4.6 TB/s: 735 instructions per row and warp with eight
+// warps per SM, which its registers allow, come next to HBM); 7777 x 2064 with a
+// gate per 1000 rows, a CTA per row, 66 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

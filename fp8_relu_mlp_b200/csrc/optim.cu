@@ -11,10 +11,11 @@
 // and sums are rounded one by one (no contraction), so the result does not
 // depend on how the loop is compiled.
 //
-// Measured over 42.5 M elements: fp32 states 213 us (30 bytes an element,
-// 6.0 TB/s), 8-bit states 178 us (18 bytes: here the 113 instructions an
-// element bound it, 15 of them random bits, 19 the rounded division and square
-// root; the SMs issue in 4 of 5 cycles), the norm 31 us (5.5 TB/s).
+// Measured over 42.5 M elements: fp32 states 211 to 220 us (30 bytes an element,
+// 6.0 to 5.8 TB/s; on BF16 weights alone 169, 24 bytes), 8-bit states 173 us (18
+// bytes: here the 113 instructions an element bound it, 15 of them random bits,
+// 19 the rounded division and square root; the SMs issue in 4 of 5 cycles), on
+// BF16 weights alone 179 (126 instructions); the norm 31 us (5.5 TB/s).
 //
 // 8-bit moments: blocks of 128 share a scale.  v is held as
 // sqrt(v), which halves the exponent range: e4m3 spans a factor 2^17.8 below
@@ -285,6 +286,8 @@ __device__ __forceinline__ void warp_step(const TensorArg& t, const StepScalars&
       if (t.p_bf16 != nullptr)
         store4<FULL>(p16 + b * 128, valid[b], make_uint2(pack_bf16x2(p[b][0], p[b][1]), pack_bf16x2(p[b][2], p[b][3])));
     } else {
+      // bits of their own: the moments use up all 32, and shared ones would tie
+      // a weight's rounding to its moments'
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = bf16_stochastic(p[b][k], mix32(bits[b][k] ^ 0x5BD1E995u) & 0xFFFFu);
