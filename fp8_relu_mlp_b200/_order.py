@@ -7,8 +7,10 @@ import torch
 
 
 def as_stream(stream, device):
-    """torch's form of a stream; an int is a handle."""
-    return stream if hasattr(stream, "wait_stream") else torch.cuda.ExternalStream(stream, device)
+    """torch's form of a stream; an int is a handle, another object has one."""
+    if hasattr(stream, "wait_stream"):
+        return stream
+    return torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device)
 
 
 def after_current(stream, device):

@@ -337,7 +337,7 @@ def test_offsets_beyond_32_bits():
     (4737, 128, 32), (9473, 64, 64),
     # fewer gate rows than workers, dealt whole; narrow gate rows of more than 32 rows, dealt whole
     (20001, 768, 30), (2500, 768, 4), (1301, 256, 1), (2601, 208, 2), (1200 * 33 + 7, 256, 32), (5000 * 50 + 11, 128, 50),
-    (9500 * 60 + 1, 16, 60)])
+    (9500 * 60 + 1, 16, 60), (1184, 768, 2), (1183, 768, 2), (18944, 16, 2), (2367, 256, 2), (9472, 64, 2), (16, 768, 2), (8, 768, 2)])
 def test_gradient_of_short_gate_rows(M, d, rows):
     p = inputs(M, d, rows, seed=M + d)
     s = saved(p, M, d, rows)

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from fp8_relu_mlp_b200 import _abi as A
+from fp8_relu_mlp_b200._order import as_stream
 from fp8_relu_mlp_b200.block import BlockScaledStack
 from fp8_relu_mlp_b200.optim import AdamW
 
@@ -154,3 +155,15 @@ def test_a_rate_that_is_not_finite_is_refused(calls, lr):
     with pytest.raises(ValueError, match="finite"):
         opt.set_lr(lr)
     assert opt.read_state()["lr"] == 0.25
+
+
+def test_streams_of_other_kinds(monkeypatch):
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, d: made.append((h, d)) or "external")
+
+    class Handle:
+        cuda_stream = 77
+    assert as_stream(5, "cuda:0") == "external" and as_stream(Handle(), "cuda:0") == "external"
+    assert made == [(5, "cuda:0"), (77, "cuda:0")]
+    own = Stream([], 3)
+    assert as_stream(own, "cuda:0") is own
